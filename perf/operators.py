@@ -97,6 +97,8 @@ def draw(rng):
                   group_v=rng.choice([16, 32, 64]), residual=rng.choice([0, 32, 128, 129]),
                   page_groups=rng.choice([0, 0, 1, 7, 16]), outliers=rng.choice([0, 0, 0, 1, 3]),
                   rope_base=rng.choice([0.0, 0.0, 0.0, 10000.0]))
+        if D == 256:                                         # what the decode's tiles hold
+            kw.update(bits=min(kw["bits"], 4), outliers=0)
     kw["batch"], nodes = _log(rng, 1, 64), _log(rng, 1, 64)
     # at most a quarter of the largest case's cached values, and its products
     top = min(131072, 64 * 8192 * 8 * 128 // 4 // (kw["batch"] * H * D))
