@@ -229,7 +229,8 @@ def _quantise(x, bits, dim, outliers):
     mn = torch.where(kept, x, math.inf).amin(dim, keepdim=True)
     mx = torch.where(kept, x, -math.inf).amax(dim, keepdim=True)
     z = _half_toward(mn, False)
-    s = _half_toward((mx - z.float()) / float(2 ** bits - 1), True)
+    # a tensor divisor: a division, where a number's would be a product with its reciprocal
+    s = _half_toward((mx - z.float()) / torch.full_like(mx, 2 ** bits - 1), True)
     sf = s.float()
     codes = ((x - z.float()) / torch.where(sf == 0, 1.0, sf)).round().clamp(0, 2 ** bits - 1)
     codes = torch.where((sf == 0) | ~kept, 0.0, codes).to(torch.uint8)
@@ -260,7 +261,8 @@ def _plain_cache(c, r):
         top = 127.0 if c["scheme"] == "int8" else 7.0
         for x in ("k", "v"):
             f = r[x].float()
-            s = f.abs().amax(-1, keepdim=True) / top
+            s = f.abs().amax(-1, keepdim=True)
+            s = s / torch.full_like(s, top)
             code = (f / torch.where(s == 0, 1.0, s)).round().clamp(-top, top).to(torch.int8)
             st[x], st[x + "s"] = code if top > 7 else _pack((code & 15).view(torch.uint8), 4), s
         return st
