@@ -320,6 +320,159 @@ int kvq_decode_attention_noalloc(const kvq_config* cfg, const void* cache, int32
                                  float softmax_scale, float* out, kvq_stream_t stream);
 
 /*
+ * kvq_tree_workspace_bytes -- device scratch needed by kvq_tree_attention for this
+ * configuration and up to `nodes` drafted tokens per sequence: a 256-byte header whose first
+ * 4 bytes are the status word, then the partial softmax results of sequences whose context
+ * is split over several blocks.  Host arithmetic only, no GPU needed.  out_bytes (host)
+ * receives the size.  Returns KVQ_OK, KVQ_ERR_ARG (nodes outside [1, KVQ_MAX_TREE_NODES])
+ * or KVQ_ERR_UNSUPPORTED (as kvq_tree_attention).
+ */
+#define KVQ_MAX_TREE_NODES 256
+int kvq_tree_workspace_bytes(const kvq_config* cfg, int32_t nodes, uint64_t* out_bytes);
+
+/*
+ * kvq_tree_attention -- one verification step of speculative decoding for every sequence of
+ * one layer: the attention of `nodes` drafted tokens over all cached tokens of their
+ * sequence and over the drafted tokens that they see.  Drafted token i of a sequence gets
+ *   o_i = sum_t p_t V_t + sum_{j seen by i} p'_j V'_j,
+ * p and p' one softmax over the cached tokens t and the seen drafts j of softmax_scale times
+ * q_i . K_t and q_i . K'_j (K, V the cache, K', V' the drafts).  The cache is not changed:
+ * the caller appends the tokens that it accepts.  The pages have no counterpart; the
+ * attention is that of kvq_decode_attention with more queries to a sequence.
+ *   cache       device, the cache (read only); cfg->in_dtype must be KVQ_DTYPE_BF16
+ *               (KVQ_ERR_UNSUPPORTED otherwise)
+ *   nodes       drafted tokens per sequence in the input rows, 1..KVQ_MAX_TREE_NODES
+ *   q           device or mapped host, bf16 [batch][nodes][q_heads][head_dim]
+ *   k_draft, v_draft
+ *               device or mapped host, bf16 [batch][nodes][kv_heads][head_dim]: the drafts'
+ *               own keys and values, not yet in the cache.  With rope_base > 0 the cached
+ *               keys are turned by their positions as in kvq_decode_attention, and q and
+ *               k_draft are passed already rotated (kvq_rope).
+ *   mask        device or mapped host, bytes [batch][nodes][nodes]: entry [b][i][j] is
+ *               nonzero where draft i sees draft j (a tree: its ancestors and itself); no
+ *               order of the nodes is assumed.  NULL: draft i sees drafts 0..i (a chain)
+ *   n_nodes     device int32 [batch] or NULL: sequence b has its first n_nodes[b] drafts
+ *               (0..nodes); the rest of its rows is padding, seen by no one, whose contents
+ *               do not matter and whose outputs are 0
+ *   out         device or mapped host, bf16 [batch][nodes][q_heads][head_dim]; a draft that
+ *               sees nothing (an empty cache and an empty mask row) gets 0
+ *   workspace   device, at least kvq_tree_workspace_bytes bytes, whose first 256 bytes are
+ *               zero before its first use; bytes 0..3 are the sticky status word
+ *               (KVQ_STATUS_TIMEOUT, KVQ_STATUS_BAD_PAGE: the output is then invalid).  It
+ *               is not the decode's workspace.  Calls that overlap on the GPU must not share
+ *               a workspace.
+ * A draft that is masked out does not reach a row, whatever its values (an infinity or a
+ * NaN in v_draft reaches the rows that see it).  Scores and sums are held in 32 bits;
+ * queries, dequantised keys and values and the softmax weights enter the matrix products
+ * rounded to binary16 (11 significant bits) under power-of-two scales, so that no value of
+ * the types' range overflows; the output is rounded to bf16 once.  All pointers 16-byte
+ * aligned (mask and n_nodes: as their type), the workspace and the cache 256-byte aligned.
+ */
+int kvq_tree_attention(const kvq_config* cfg, const void* cache, int32_t layer, int32_t nodes, const void* q,
+                       const void* k_draft, const void* v_draft, const uint8_t* mask, const int32_t* n_nodes,
+                       float softmax_scale, void* out, void* workspace, uint64_t workspace_bytes,
+                       kvq_stream_t stream);
+
+/*
+ * kvq_read_tokens -- read cached tokens of one layer back: for the sequences [seq_begin,
+ * seq_begin + seq_count), `count` tokens each from token `first` (or starts[i]) on, as the
+ * values that the decode attends over ("Quantizing the KV cache", "Per-channel and per-token
+ * grouping": the dequantised value): code * scale + zero for KIVI groups, the window's bf16
+ * values, an outlier's bf16 value, code * scale for the other schemes -- binary32, a product
+ * and then a sum -- rounded to nearest even where out_dtype is KVQ_DTYPE_BF16.
+ *   cache        device; its status word gets KVQ_STATUS_BAD_PAGE where a token's
+ *                block-table entry is outside the pool (the token reads as 0)
+ *   starts       device int32 [seq_count] or NULL: the first token of each sequence (a
+ *                negative one is taken as it is: the tokens before 0 read as 0)
+ *   first        the first token of every sequence where starts is NULL (>= 0)
+ *   count        tokens per sequence in the output rows (>= 0)
+ *   k_out, v_out device or mapped host, [seq_count][count][kv_heads][head_dim] in out_dtype
+ *                (kvq_dtype); either may be NULL.  Rows of tokens that the sequence does not
+ *                hold are 0.
+ * Keys of caches with rope_base > 0 come back as they were appended, before the rotation
+ * (kvq_rope turns them).  Enqueued on `stream`.
+ */
+int kvq_read_tokens(const kvq_config* cfg, void* cache, int32_t layer, int32_t seq_begin, int32_t seq_count,
+                    const int32_t* starts, int32_t first, int32_t count, void* k_out, void* v_out,
+                    int32_t out_dtype, kvq_stream_t stream);
+
+/*
+ * Rotary positions.  The first rotary_dim channels of a head are turned in pairs (x, y) by
+ * the angle a_i = t * w_i of position t, the binary32 product of t (as binary32) and the
+ * pair's binary32 frequency -- the angle that the decode turns the keys of a pre-RoPE cache
+ * by ("KVQuant: Towards 10 Million Context Length ...", "Key points") -- into
+ *   (m (x cos a - y sin a), m (y cos a + x sin a)),
+ * the other channels are copied.  Arithmetic in binary32, rounded once to dtype.
+ *   head_dim         channels per head (1..1024)
+ *   rotary_dim       channels turned, even, 2..min(head_dim, KVQ_MAX_ROTARY_DIM)
+ *   layout           kvq_rope_layout: which channels make pair i
+ *   dtype            kvq_dtype of the rows
+ *   scaling          kvq_rope_scaling, base, factor, low, high, original_context: how
+ *                    kvq_rope_frequencies fills w
+ *   magnitude        m (1 for a plain rotation)
+ */
+#define KVQ_MAX_ROTARY_DIM 256
+enum kvq_rope_layout {
+    KVQ_ROPE_HALF = 0,        /* channels i and i + rotary_dim / 2 */
+    KVQ_ROPE_INTERLEAVED = 1  /* channels 2 i and 2 i + 1 */
+};
+enum kvq_rope_scaling {
+    KVQ_ROPE_SCALE_NONE = 0,    /* w_i = base^(-2 i / rotary_dim) */
+    KVQ_ROPE_SCALE_LINEAR = 1,  /* w_i / factor: positions interpolated */
+    KVQ_ROPE_SCALE_NTK = 2,     /* base * factor^(rotary_dim / (rotary_dim - 2)) for base;
+                                   rotary_dim >= 4 */
+    KVQ_ROPE_SCALE_BY_PARTS = 3 /* g w_i + (1 - g) w_i / factor, g = clamp((r - low) / (high -
+                                   low), 0, 1) of the turns r = original_context w_i / (2 pi):
+                                   fast pairs kept, slow pairs interpolated */
+};
+enum kvq_rope_flags {
+    KVQ_ROPE_TRANSPOSE = 1u  /* multiply by the transposed matrix (the angle's sign turned): the
+                                gradient of the rotation's input from that of its output */
+};
+typedef struct kvq_rope_config {
+    int32_t head_dim;
+    int32_t rotary_dim;
+    int32_t layout;
+    int32_t dtype;
+    int32_t scaling;
+    int32_t original_context;
+    float base;
+    float factor;
+    float low;
+    float high;
+    float magnitude;
+} kvq_rope_config;
+
+/*
+ * kvq_rope_frequencies -- fills w (host, rotary_dim / 2 floats) with the pairs' frequencies,
+ * computed in binary64 and rounded to binary32 once.  Host arithmetic only.  Returns KVQ_OK or
+ * KVQ_ERR_ARG (base not above 0; with a scaling, factor not above 0; by parts, high not above
+ * low or original_context below 1; anything not finite).
+ */
+int kvq_rope_frequencies(const kvq_rope_config* rope, float* w);
+
+/*
+ * kvq_rope -- turns the heads of `tokens` rows of queries and of keys by their positions.
+ *   w            host, rotary_dim / 2 frequencies (kvq_rope_frequencies, or the caller's
+ *                own); read before the call returns
+ *   positions    device or mapped host, int32 [tokens]
+ *   q, k         device or mapped host, `tokens` rows of q_heads (kv_heads) heads in dtype,
+ *                one head after another; row i starts q_stride (k_stride) elements after row
+ *                i - 1, so a row may be part of a fused projection's.  k may be NULL with
+ *                kv_heads 0, and q with q_heads 0.
+ *   q_out, k_out the results, in rows of their own strides; each either the input itself
+ *                with the same stride (in place) or apart from both inputs.  Only the heads'
+ *                channels are written.
+ *   flags        KVQ_ROPE_TRANSPOSE or 0
+ * Pointers must be aligned to their element.  No two rows of an output may overlap: a stride
+ * is at least heads * head_dim (KVQ_ERR_ARG otherwise; not asked where tokens is below 2).
+ * One kernel on `stream`.
+ */
+int kvq_rope(const kvq_rope_config* rope, const float* w, const int32_t* positions, int64_t tokens, const void* q,
+             void* q_out, int32_t q_heads, int64_t q_stride, int64_t q_out_stride, const void* k, void* k_out,
+             int32_t kv_heads, int64_t k_stride, int64_t k_out_stride, uint32_t flags, kvq_stream_t stream);
+
+/*
  * kvq_read_status -- OR of the status words of `cache` and `workspace` (either may be
  * NULL) into *out (host).  Synchronises `stream` to read them.  The pages define no error
  * reporting; the status bits name the conditions the pages' method leaves open on a

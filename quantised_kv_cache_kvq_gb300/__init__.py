@@ -1,5 +1,7 @@
-"""GB300 quantised KV cache: packed KIVI / INT8 / FP8 caches and single-query decode
-attention over them, in CUDA kernels behind the C ABI of include/kvq.h.
+"""GB300 quantised KV cache: packed KIVI / INT8 / FP8 caches, single-query decode attention
+over them and what speculative decoding needs next to it (attention of drafted tokens over
+a cache, reading a cache back, rotary positions), in CUDA kernels behind the C ABI of
+include/kvq.h.
 
 `QuantizedKVCache` is a convenience holder: it allocates the cache and the decode
 workspace as torch device tensors (torch serves only as the device allocator and stream
@@ -12,10 +14,12 @@ from ._native import (  # noqa: F401
     KVQ_NO_AUTOFLUSH, KVQ_SCHEME_FP8_E4M3, KVQ_SCHEME_FP8_E5M2, KVQ_SCHEME_INT4, KVQ_SCHEME_INT8,
     KVQ_SCHEME_KIVI,
     KVQ_STATUS_BAD_PAGE, KVQ_STATUS_CAPACITY, KVQ_STATUS_NONFINITE, KVQ_STATUS_RING_FULL, KVQ_STATUS_TIMEOUT,
-    KvqConfig, KvqError, kvq_cache_bytes, kvq_cache_init, kvq_decode_attention,
+    KVQ_MAX_ROTARY_DIM, KVQ_MAX_TREE_NODES, KVQ_ROPE_HALF, KVQ_ROPE_INTERLEAVED, KVQ_ROPE_SCALE_BY_PARTS,
+    KVQ_ROPE_SCALE_LINEAR, KVQ_ROPE_SCALE_NONE, KVQ_ROPE_SCALE_NTK, KVQ_ROPE_TRANSPOSE,
+    KvqConfig, KvqError, KvqRopeConfig, kvq_cache_bytes, kvq_cache_init, kvq_decode_attention,
     kvq_decode_attention_noalloc,
-    kvq_flush_group, kvq_quantize_append, kvq_read_status, kvq_sequence_lengths,
-    kvq_workspace_bytes, library_path, load, status_string,
+    kvq_flush_group, kvq_quantize_append, kvq_read_status, kvq_read_tokens, kvq_rope, kvq_rope_frequencies,
+    kvq_sequence_lengths, kvq_tree_attention, kvq_tree_workspace_bytes, kvq_workspace_bytes, library_path, load, status_string,
 )
 
 _SCHEMES = {"kivi": KVQ_SCHEME_KIVI, "int8": KVQ_SCHEME_INT8, "fp8": KVQ_SCHEME_FP8_E4M3,
@@ -49,6 +53,19 @@ def max_pages(cfg) -> int:
     return (ng + cfg.page_groups - 1) // cfg.page_groups if cfg.page_groups > 0 else 0
 
 
+def _expect(name, x, shape, dtype, device):
+    """Refuses a tensor that the library would read wrongly."""
+    kinds = dtype if isinstance(dtype, tuple) else (dtype,)
+    if tuple(x.shape) != tuple(shape) or x.dtype not in kinds or not x.is_contiguous():
+        raise ValueError("%s: expected a contiguous %s tensor of shape %s, got %s %s%s" % (
+            name, " or ".join(str(k) for k in kinds), tuple(shape), x.dtype, tuple(x.shape),
+            "" if x.is_contiguous() else " (not contiguous)"))
+    if x.is_cuda and x.device != device:
+        raise ValueError("%s is on %s, not on %s" % (name, x.device, device))
+    if not x.is_cuda and x.numel() and not x.is_pinned():
+        raise ValueError("%s: host memory must be page-locked" % name)
+
+
 class QuantizedKVCache:
     """A cache and its decode workspace on one GPU."""
 
@@ -57,10 +74,13 @@ class QuantizedKVCache:
         load()
         self.cfg = cfg
         self.device = torch.device(device)
+        if self.device.type == "cuda" and self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
         self.nbytes = kvq_cache_bytes(cfg, cfg.max_tokens, KVQ_BYTES_LAYOUT)
         self.cache = torch.empty(self.nbytes, dtype=torch.uint8, device=self.device)
         kvq_cache_init(cfg, self.cache)
         self.workspace = torch.zeros(kvq_workspace_bytes(cfg), dtype=torch.uint8, device=self.device)
+        self._tree_workspaces = {}
 
     def append(self, layer, k_new, v_new, seq_begin=0, n_valid=None, fp8_scales=None, flags=0,
                stream=None):
@@ -83,8 +103,77 @@ class QuantizedKVCache:
                              stream=stream)
         return out
 
+    def tree_workspace(self, nodes):
+        """Scratch for tree_decode calls of up to `nodes` drafts: one per set of calls that may
+        overlap on the GPU (and one per CUDA graph that may be replayed beside another)."""
+        import torch
+        return torch.zeros(kvq_tree_workspace_bytes(self.cfg, nodes), dtype=torch.uint8, device=self.device)
+
+    def tree_decode(self, layer, q, k_draft, v_draft, mask=None, n_nodes=None, softmax_scale=None, out=None,
+                    workspace=None, stream=None):
+        """Attention of drafted tokens over the cached tokens and the drafts that they see.
+        q: bf16 [batch][nodes][q_heads][head_dim]; k_draft, v_draft: bf16 [batch][nodes]
+        [kv_heads][head_dim]; mask: bool or uint8 [batch][nodes][nodes] (None: a chain);
+        n_nodes: int32 [batch] or None.  Returns bf16 [batch][nodes][q_heads][head_dim].
+        workspace: tree_workspace(nodes), by default one that the cache keeps for each number
+        of nodes."""
+        import torch
+        c = self.cfg
+        nodes = q.shape[1] if q.dim() == 4 else 0
+        bf16 = torch.bfloat16
+        _expect("q", q, (c.batch, nodes, c.q_heads, c.head_dim), bf16, self.device)
+        _expect("k_draft", k_draft, (c.batch, nodes, c.kv_heads, c.head_dim), bf16, self.device)
+        _expect("v_draft", v_draft, (c.batch, nodes, c.kv_heads, c.head_dim), bf16, self.device)
+        if mask is not None:
+            _expect("mask", mask, (c.batch, nodes, nodes), (torch.bool, torch.uint8), self.device)
+        if n_nodes is not None:
+            _expect("n_nodes", n_nodes, (c.batch,), torch.int32, self.device)
+        with torch.cuda.device(self.device):
+            if workspace is None:
+                workspace = self._tree_workspaces.get(nodes)
+                if workspace is None:
+                    workspace = self._tree_workspaces[nodes] = self.tree_workspace(nodes)
+            if out is None:
+                out = torch.empty_like(q)
+            else:
+                _expect("out", out, q.shape, bf16, self.device)
+            kvq_tree_attention(c, self.cache, layer, nodes, q, k_draft, v_draft, mask, n_nodes,
+                               1.0 / math.sqrt(c.head_dim) if softmax_scale is None else softmax_scale, out,
+                               workspace, stream=stream)
+        return out
+
+    def read(self, layer, first=0, count=None, seq_begin=0, seq_count=None, dtype="bf16", k_out=None, v_out=None,
+             stream=None):
+        """Cached tokens [first, first + count) of sequences [seq_begin, seq_begin + seq_count),
+        dequantised: (keys, values) [seq_count][count][kv_heads][head_dim], bf16 or f32; rows
+        past a sequence's tokens are 0.  first: a number, or a device int32 tensor [seq_count];
+        count: by default up to the capacity."""
+        import torch
+        c = self.cfg
+        starts = first if isinstance(first, torch.Tensor) else None
+        if seq_count is None:
+            seq_count = c.batch - seq_begin
+        if starts is not None:
+            _expect("first", starts, (seq_count,), torch.int32, self.device)
+            first = 0
+        if count is None:
+            count = c.max_tokens - first
+        code = {"bf16": KVQ_DTYPE_BF16, "f32": KVQ_DTYPE_F32}[dtype]
+        kind = torch.float32 if code == KVQ_DTYPE_F32 else torch.bfloat16
+        shape = (seq_count, count, c.kv_heads, c.head_dim)
+        with torch.cuda.device(self.device):
+            outs = [torch.empty(shape, dtype=kind, device=self.device) if x is None else x for x in (k_out, v_out)]
+            _expect("k_out", outs[0], shape, kind, self.device)
+            _expect("v_out", outs[1], shape, kind, self.device)
+            kvq_read_tokens(c, self.cache, layer, seq_begin, seq_count, starts, first, count, outs[0], outs[1], code,
+                            stream)
+        return outs[0], outs[1]
+
     def status(self, stream=None):
-        return kvq_read_status(self.cache, self.workspace, stream)
+        word = kvq_read_status(self.cache, self.workspace, stream)
+        for ws in self._tree_workspaces.values():
+            word |= kvq_read_status(None, ws, stream)
+        return word
 
     def lengths(self, layer, stream=None):
         import torch
@@ -92,3 +181,63 @@ class QuantizedKVCache:
         qn = torch.empty(self.cfg.batch, dtype=torch.int32, device=self.device)
         kvq_sequence_lengths(self.cfg, self.cache, layer, n, qn, stream)
         return n, qn
+
+
+_ROPE_LAYOUTS = {"half": KVQ_ROPE_HALF, "interleaved": KVQ_ROPE_INTERLEAVED}
+_ROPE_SCALINGS = {"none": KVQ_ROPE_SCALE_NONE, "linear": KVQ_ROPE_SCALE_LINEAR, "ntk": KVQ_ROPE_SCALE_NTK,
+                  "by_parts": KVQ_ROPE_SCALE_BY_PARTS}
+
+
+class RotaryEmbedding:
+    """Rotary positions of queries and keys (kvq_rope_config names the parameters; the
+    frequencies are computed once, here).  For a cache with rope_base the queries and the
+    drafts' keys are turned with the same base, all of a head, layout "half"."""
+
+    def __init__(self, head_dim, base=10000.0, rotary_dim=None, layout="half", scaling="none", factor=1.0, low=1.0,
+                 high=4.0, original_context=8192, magnitude=1.0):
+        self.rope = KvqRopeConfig(
+            head_dim=head_dim, rotary_dim=head_dim if rotary_dim is None else rotary_dim, layout=_ROPE_LAYOUTS[layout],
+            dtype=KVQ_DTYPE_BF16, scaling=_ROPE_SCALINGS[scaling], original_context=original_context, base=base,
+            factor=factor, low=low, high=high, magnitude=magnitude)
+        self.frequencies = kvq_rope_frequencies(self.rope)
+        self._f32 = KvqRopeConfig.from_buffer_copy(self.rope)
+        self._f32.dtype = KVQ_DTYPE_F32
+
+    def rotate(self, q, k, positions, q_out=None, k_out=None, transpose=False, stream=None):
+        """q, k: [tokens][heads][head_dim], bf16 or float32 (one of them may be None), each
+        token's heads one after another, the tokens at any stride (slices of a fused
+        projection); positions: int32 [tokens].  Returns (q, k) turned, in new tensors or in
+        q_out, k_out (q and k themselves: in place).  transpose: the gradient."""
+        import torch
+        given = [(n, x) for n, x in (("q", q), ("k", k)) if x is not None]
+        if not given:
+            raise ValueError("rotate: neither q nor k")
+        dtype, device, tokens = given[0][1].dtype, given[0][1].device, given[0][1].shape[0]
+        if dtype not in (torch.bfloat16, torch.float32) or device.type != "cuda":
+            raise ValueError("rotate: expected bfloat16 or float32 rows on a GPU, got %s on %s" % (dtype, device))
+        _expect("positions", positions, (tokens,), torch.int32, device)
+        args, outs = [], []
+        with torch.cuda.device(device):
+            for name, x, y in (("q", q, q_out), ("k", k, k_out)):
+                if x is None:
+                    args += [None, None, 0, 0, 0]
+                    outs.append(None)
+                    continue
+                if y is None:
+                    y = torch.empty(x.shape, dtype=dtype, device=device)
+                for n, z in ((name, x), (name + "_out", y)):
+                    self._rows(n, z, x.shape, tokens, dtype, device)
+                args += [x, y, x.shape[1], x.stride(0), y.stride(0)]
+                outs.append(y)
+            kvq_rope(self.rope if dtype == torch.bfloat16 else self._f32, self.frequencies, positions, tokens, *args,
+                     flags=KVQ_ROPE_TRANSPOSE if transpose else 0, stream=stream)
+        return outs[0], outs[1]
+
+    def _rows(self, name, x, shape, tokens, dtype, device):
+        D = self.rope.head_dim
+        if x.dim() != 3 or x.shape != shape or x.shape[0] != tokens or x.shape[2] != D or x.dtype != dtype \
+                or x.device != device:
+            raise ValueError("%s: expected %s [%d][heads][%d] on %s, got %s %s on %s" % (
+                name, dtype, tokens, D, device, x.dtype, tuple(x.shape), x.device))
+        if x.numel() and (x.stride(2) != 1 and D > 1 or x.stride(1) != D and x.shape[1] > 1):
+            raise ValueError("%s: a token's heads must lie one after another" % name)

@@ -14,12 +14,18 @@ KVQ_OK, KVQ_ERR_ARG, KVQ_ERR_ALIGN, KVQ_ERR_CAPACITY = 0, -1, -2, -3
 KVQ_ERR_WORKSPACE, KVQ_ERR_CUDA, KVQ_ERR_UNSUPPORTED = -4, -5, -6
 KVQ_STATUS_CAPACITY, KVQ_STATUS_RING_FULL, KVQ_STATUS_NONFINITE, KVQ_STATUS_TIMEOUT = 1, 2, 4, 8
 KVQ_STATUS_BAD_PAGE = 16
+KVQ_ROPE_HALF, KVQ_ROPE_INTERLEAVED = 0, 1
+KVQ_ROPE_SCALE_NONE, KVQ_ROPE_SCALE_LINEAR, KVQ_ROPE_SCALE_NTK, KVQ_ROPE_SCALE_BY_PARTS = 0, 1, 2, 3
+KVQ_ROPE_TRANSPOSE = 1
+KVQ_MAX_TREE_NODES = 256
+KVQ_MAX_ROTARY_DIM = 256
 
 # every symbol include/kvq.h declares
 EXPORTS = (
     "kvq_cache_bytes", "kvq_cache_init", "kvq_quantize_append", "kvq_flush_group",
     "kvq_workspace_bytes", "kvq_decode_attention", "kvq_decode_attention_noalloc", "kvq_read_status",
     "kvq_sequence_lengths", "kvq_status_string",
+    "kvq_tree_workspace_bytes", "kvq_tree_attention", "kvq_read_tokens", "kvq_rope_frequencies", "kvq_rope",
 )
 KVQ_NOALLOC_SCRATCH_BYTES = 16 << 20
 KVQ_MAX_DECODE_BLOCKS = 2048
@@ -41,6 +47,12 @@ class KvqConfig(C.Structure):
         (kept alive here) or None."""
         self._table = table
         self.block_table = None if table is None else int(table.data_ptr())
+
+
+class KvqRopeConfig(C.Structure):
+    """struct kvq_rope_config"""
+    _fields_ = [(n, C.c_int32) for n in ("head_dim", "rotary_dim", "layout", "dtype", "scaling", "original_context")] + [
+        (n, C.c_float) for n in ("base", "factor", "low", "high", "magnitude")]
 
 
 class KvqError(RuntimeError):
@@ -78,6 +90,12 @@ def load():
         "kvq_decode_attention_noalloc": [cfgp, P, i32, P, C.c_float, P, P],
         "kvq_read_status": [P, P, C.POINTER(u32), P],
         "kvq_sequence_lengths": [cfgp, P, i32, P, P, P],
+        "kvq_tree_workspace_bytes": [cfgp, i32, C.POINTER(u64)],
+        "kvq_tree_attention": [cfgp, P, i32, i32, P, P, P, P, P, C.c_float, P, P, u64, P],
+        "kvq_read_tokens": [cfgp, P, i32, i32, i32, P, i32, i32, P, P, i32, P],
+        "kvq_rope_frequencies": [C.POINTER(KvqRopeConfig), C.POINTER(C.c_float)],
+        "kvq_rope": [C.POINTER(KvqRopeConfig), C.POINTER(C.c_float), P, i64, P, P, i32, i64, i64, P, P, i32, i64, i64,
+                     u32, P],
     }
     for name, args in sig.items():
         fn = getattr(L, name)
@@ -169,3 +187,41 @@ def kvq_read_status(cache=None, workspace=None, stream=None):
 def kvq_sequence_lengths(cfg, cache, layer, n_out=None, qn_out=None, stream=None):
     _check("kvq_sequence_lengths", load().kvq_sequence_lengths(
         C.byref(cfg), _ptr(cache), int(layer), _ptr(n_out), _ptr(qn_out), _stream(stream)))
+
+
+def kvq_tree_workspace_bytes(cfg, nodes):
+    out = C.c_uint64(0)
+    _check("kvq_tree_workspace_bytes", load().kvq_tree_workspace_bytes(C.byref(cfg), int(nodes), C.byref(out)))
+    return out.value
+
+
+def kvq_tree_attention(cfg, cache, layer, nodes, q, k_draft, v_draft, mask, n_nodes, softmax_scale, out, workspace,
+                       workspace_bytes=None, stream=None):
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    _check("kvq_tree_attention", load().kvq_tree_attention(
+        C.byref(cfg), _ptr(cache), int(layer), int(nodes), _ptr(q), _ptr(k_draft), _ptr(v_draft), _ptr(mask),
+        _ptr(n_nodes), float(softmax_scale), _ptr(out), _ptr(workspace), int(workspace_bytes), _stream(stream)))
+
+
+def kvq_read_tokens(cfg, cache, layer, seq_begin, seq_count, starts, first, count, k_out, v_out,
+                    out_dtype=KVQ_DTYPE_BF16, stream=None):
+    _check("kvq_read_tokens", load().kvq_read_tokens(
+        C.byref(cfg), _ptr(cache), int(layer), int(seq_begin), int(seq_count), _ptr(starts), int(first), int(count),
+        _ptr(k_out), _ptr(v_out), int(out_dtype), _stream(stream)))
+
+
+def kvq_rope_frequencies(rope):
+    """The pairs' frequencies as a ctypes float array (rotary_dim / 2)."""
+    w = (C.c_float * max(1, min(rope.rotary_dim, KVQ_MAX_ROTARY_DIM) // 2))()
+    _check("kvq_rope_frequencies", load().kvq_rope_frequencies(C.byref(rope), w))
+    return w
+
+
+def kvq_rope(rope, w, positions, tokens, q, q_out, q_heads, q_stride, q_out_stride, k=None, k_out=None, kv_heads=0,
+             k_stride=0, k_out_stride=0, flags=0, stream=None):
+    """w: ctypes float array (kvq_rope_frequencies); strides in elements."""
+    _check("kvq_rope", load().kvq_rope(
+        C.byref(rope), w, _ptr(positions), int(tokens), _ptr(q), _ptr(q_out), int(q_heads), int(q_stride),
+        int(q_out_stride), _ptr(k), _ptr(k_out), int(kv_heads), int(k_stride), int(k_out_stride), int(flags),
+        _stream(stream)))

@@ -51,6 +51,9 @@ UNITS = {
     "kvq_decode_fp8.cu": [],
     "kvq_decode_rope.cu": [],
     "kvq_noalloc.cu": [],
+    "kvq_rotary.cu": [],
+    "kvq_read.cu": [],
+    "kvq_tree.cu": [],
 }
 
 

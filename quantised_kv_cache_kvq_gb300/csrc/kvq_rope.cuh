@@ -8,6 +8,8 @@
 // Included by kvq_decode.cuh after the helpers it uses.
 #pragma once
 
+#include "kvq_rope_angle.cuh"
+
 namespace kvq {
 
 // Bit, within a group record's value codes, of the code of (token t of the group, channel
@@ -35,25 +37,6 @@ __device__ __forceinline__ int code_at(const uint8_t* p, int bit) {
 __device__ __forceinline__ float half_at(const uint8_t* p, int byte) {
     return __half2float(*reinterpret_cast<const __half*>(p + byte));
 }
-// cos and sin of a binary32 angle a.  For |a| < 2^17, Cody and Waite's reduction by 2 pi
-// in three binary32 parts (the first, 6.28125, has 8 significant bits, so k * C1 is exact
-// for the |k| < 2^15 that occur; C2 and C3 carry the rest of 2 pi), then the hardware sine
-// and cosine on the reduced |r| <= pi (absolute error about 1e-6).  Larger angles take the
-// library's sincosf with its full argument reduction.
-__device__ __forceinline__ void rope_sincos(float a, float* sn, float* cs) {
-    if (fabsf(a) < 131072.0f) {
-        constexpr float kInv2Pi = 0.159154943091895336f;
-        constexpr float C1 = 6.28125f, C2 = 1.9353072e-3f, C3 = 1.0253132e-11f;
-        const float k = rintf(a * kInv2Pi);
-        float r = fmaf(-k, C1, a);
-        r = fmaf(-k, C2, r);
-        r = fmaf(-k, C3, r);
-        __sincosf(r, sn, cs);
-    } else {
-        sincosf(a, sn, cs);
-    }
-}
-
 // Dequantised value of a code: code * scale + zero, a binary32 product, then a sum.
 __device__ __forceinline__ float dequant(int code, float s, float z) {
     return __fadd_rn(__fmul_rn(static_cast<float>(code), s), z);
