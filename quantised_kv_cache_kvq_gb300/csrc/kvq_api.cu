@@ -196,7 +196,11 @@ int decode_blocks(const void* fn, int threads, int64_t smem, int* nb) {
                 return KVQ_OK;
             }
     }
-    if (smem > 48 * 1024 &&
+    // the limit is only ever raised: a kernel runs with the shared memory of several layouts, and
+    // the sizes remembered above are launched without coming here again
+    cudaFuncAttributes attr;
+    if (cudaFuncGetAttributes(&attr, fn) != cudaSuccess) return KVQ_ERR_CUDA;
+    if (smem > attr.maxDynamicSharedSizeBytes &&
         cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
         return KVQ_ERR_CUDA;
     int per_sm = 0;

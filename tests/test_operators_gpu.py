@@ -262,15 +262,15 @@ def test_tree_of_one_draft_is_the_decode_after_its_append(K):
     p, gen = make(dict(bits=2, lengths=(300, 64), max_tokens=320))
     q, dk, dv, _ = drafts(p, 1, gen, tree=False)
     tree = check_tree(K, p, q, dk, dv, None)[:, 0]
+    ref, tol = (x[:, 0] for x in tree64(p, 0, q, dk, dv, None, None, 1.0 / math.sqrt(128)))
     p.append(0, dk, dv)
     out = torch.empty(q.shape[0], *q.shape[2:], device="cuda")
     K.kvq_decode_attention(p.lib_cfg, p.gpu, 0, q[:, 0].contiguous().cuda(), 1.0 / math.sqrt(128), out, p.ws)
-    # the append leaves the draft in the window unless it completes a group: the decode's own
-    # tolerance and one bf16 step
-    ref = out.cpu().numpy()
-    flushed = [p.img.state(0, b)[1] for b in range(2)]
-    assert flushed == [256, 32]
-    assert (np.abs(tree - ref) <= 2e-3 + 1.4e-2 * np.abs(ref)).all()
+    # the append leaves the draft in the window (no group completes), so both compute the same
+    # attention: the tree is within its bound of the 64-bit value (check_tree), the decode within
+    # its own tolerance, and so the two within their sum of each other
+    assert [p.img.state(0, b)[1] for b in range(2)] == [256, 32]
+    assert (np.abs(tree - out.cpu().numpy()) <= tol + 2e-3 + 1e-2 * np.abs(ref)).all()
 
 
 def test_tree_masks_padding_and_empty_rows(K):
@@ -425,6 +425,18 @@ def test_tree_reports_a_page_outside_the_pool(K):
     got = cache.tree_decode(0, q.cuda(), dk.cuda(), dv.cuda(), mask.cuda()).float().cpu().numpy()
     assert cache.status() == K.KVQ_STATUS_BAD_PAGE
     assert np.array_equal(got[0], good[0].astype(np.float32))
+
+
+@pytest.mark.parametrize("op", ["decode", "tree"])
+def test_layouts_that_share_a_kernel_take_turns(K, op):
+    """A layout with more shared memory than the one that ran in between launches again."""
+    pairs = [make(dict(bits=4, group_k=g, group_v=128, lengths=(300,), max_tokens=320, residual=16)) for g in (128, 80)]
+    for p, gen in pairs + pairs:
+        if op == "decode":
+            got, ref = p.decode(0, p.rand_q(gen))
+            assert (np.abs(got - ref) <= 2e-3 + 1e-2 * np.abs(ref)).all()
+        else:
+            check_tree(K, p, *drafts(p, 3, gen))
 
 
 # ------------------------------------------------------------------------------ rotary positions
