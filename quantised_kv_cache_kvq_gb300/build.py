@@ -54,6 +54,10 @@ UNITS = {
     "kvq_rotary.cu": [],
     "kvq_read.cu": [],
     "kvq_tree.cu": [],
+    "kvq_tree_d32.cu": [],
+    "kvq_tree_d64.cu": [],
+    "kvq_tree_d128.cu": [],
+    "kvq_tree_d256.cu": [],
 }
 
 

@@ -2,102 +2,62 @@
 #include <cmath>
 #include <cstdint>
 
-#include "kvq_elements.cuh"
 #include "kvq_internal.cuh"
 #include "kvq_launch.h"
-#include "kvq_rope_angle.cuh"
+#include "kvq_tree.cuh"
 
 namespace kvq {
 namespace {
 
-constexpr int kTreeThreads = 256;
-
-struct TreeArgs {
+struct TreePlan {
     Layout lo;
-    const uint8_t* cache;
-    int layer, nodes;
-    const __nv_bfloat16 *q, *k, *v;
-    const uint8_t* mask;
-    const int32_t* n_nodes;
-    float scale;
-    __nv_bfloat16* out;
-    uint8_t* ws;
-    float rope_w[128];
+    int N, RT, rows, TT, staged;
+    int64_t stage, ml_off, o_off, bytes;
 };
 
-// A block per (node, query head, sequence): its 8 warps take the tokens in turn, each with a
-// running maximum and sum (one pass over the data), joined at the end.
-__global__ void __launch_bounds__(kTreeThreads) k_tree(TreeArgs a) {
-    __shared__ float so[8][256], sm[8], sl[8];
-    const Layout& lo = a.lo;
-    const int D = lo.D, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int i = blockIdx.x, hq = blockIdx.y, b = blockIdx.z, h = hq / lo.gqa;
-    const int32_t* st = state_ptr(lo, a.cache, a.layer, b);
-    const int n = st[0], qn = st[1];
-    int nodes = a.n_nodes ? a.n_nodes[b] : a.nodes;
-    nodes = nodes < 0 ? 0 : (nodes > a.nodes ? a.nodes : nodes);
-    const int64_t row = (((int64_t)b * a.nodes + i) * lo.Hq + hq) * D;
-    float m = -INFINITY, l = 0.0f, o[8] = {}, q[8];
-    bool bad = false;
-    for (int e = 0; e < D / 32; ++e) q[e] = __bfloat162float(a.q[row + lane + 32 * e]);
-    if (i < nodes)
-        for (int64_t t = warp; t < n + nodes; t += 8) {
-            const int64_t j = t - n;
-            if (j >= 0 && !(a.mask ? a.mask[((int64_t)b * a.nodes + i) * a.nodes + j] != 0 : j <= i)) continue;
-            const int64_t drow = (((int64_t)b * a.nodes + j) * lo.H + h) * D;
-            float s = 0.0f, v[8];
-            for (int e = 0; e < D / 32; ++e) {
-                const int c = lane + 32 * e;
-                float k;
-                if (j >= 0) {
-                    k = __bfloat162float(a.k[drow + c]);
-                    v[e] = __bfloat162float(a.v[drow + c]);
-                } else {
-                    k = cached_element(lo, a.cache, a.layer, b, h, qn, t, c, 0, &bad);
-                    v[e] = cached_element(lo, a.cache, a.layer, b, h, qn, t, c, 1, &bad);
-                    if (lo.rope_base > 0.0f) {
-                        const int other = c < D / 2 ? c + D / 2 : c - D / 2;
-                        const float y = cached_element(lo, a.cache, a.layer, b, h, qn, t, other, 0, &bad);
-                        float sn, cs;
-                        rope_sincos(__fmul_rn(static_cast<float>(t), a.rope_w[c % (D / 2)]), &sn, &cs);
-                        k = c < D / 2 ? k * cs - y * sn : k * cs + y * sn;
-                    }
-                }
-                s = fmaf(q[e], k, s);
-            }
-            for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-            s *= a.scale;
-            const float m2 = fmaxf(m, s), f = exp2f(m - m2), p = exp2f(s - m2);
-            m = m2;
-            l = l * f + p;
-            for (int e = 0; e < D / 32; ++e) o[e] = fmaf(p, v[e], o[e] * f);
-        }
-    if (bad) atomicOr(reinterpret_cast<uint32_t*>(a.ws), KVQ_STATUS_BAD_PAGE);
-    if (lane == 0) {
-        sm[warp] = m;
-        sl[warp] = l;
-    }
-    for (int e = 0; e < D / 32; ++e) so[warp][lane + 32 * e] = o[e];
-    __syncthreads();
-    for (int c = threadIdx.x; c < D; c += kTreeThreads) {
-        float M = -INFINITY, L = 0.0f, O = 0.0f;
-        for (int w = 0; w < 8; ++w) M = fmaxf(M, sm[w]);
-        for (int w = 0; w < 8; ++w) {
-            if (sl[w] == 0.0f) continue;
-            const float f = exp2f(sm[w] - M);
-            L += sl[w] * f;
-            O += so[w][c] * f;
-        }
-        a.out[row + c] = __float2bfloat16_rn(L != 0.0f ? O / L : 0.0f);
-    }
-}
+// Bytes of the operand tiles of k_tree<N, D> (TreeSmem), and what a block may have next to the
+// kernel's static arrays (under 6 KiB).
+int64_t tile_bytes(int N, int D) { return 256 * D + (D > 128 ? 65536 : 32768) + 2 * N * D + 256 * N; }
+constexpr int64_t kTreeSmemLimit = 221 * 1024;
 
-int tree_plan(const kvq_config* cfg, int nodes, Layout* lo, int64_t* bytes) {
-    const int rc = make_layout(cfg, cfg->max_tokens, lo);
+// The row tile: the fewest columns, 16 to 128, that hold all queries of a KV head, or 128 (64
+// for heads of 256 channels, whose tiles are twice as large).  The packed bytes of a tile pass
+// through shared memory where they fit next to the operand tiles; with half the columns if
+// that makes the room; else (KIVI records of 256 channels at 8 bits or with outliers) the
+// kernel reads them in place.
+int tree_plan(const kvq_config* cfg, int nodes, TreePlan* p) {
+    const int rc = make_layout(cfg, cfg->max_tokens, &p->lo);
     if (rc != KVQ_OK) return rc;
+    const Layout& lo = p->lo;
     if (nodes < 1 || nodes > KVQ_MAX_TREE_NODES) return KVQ_ERR_ARG;
-    if (lo->dtype != KVQ_DTYPE_BF16) return KVQ_ERR_UNSUPPORTED;
-    *bytes = 256;
+    if (lo.dtype != KVQ_DTYPE_BF16) return KVQ_ERR_UNSUPPORTED;
+    const int D = lo.D;
+    p->rows = nodes * lo.gqa;
+    p->N = 16;
+    while (p->N < p->rows && p->N < (D > 128 ? 64 : 128)) p->N *= 2;
+    if (lo.scheme == KVQ_SCHEME_KIVI) {
+        p->TT = 128 / lo.G * lo.G;
+        p->stage = (int64_t)(128 / lo.G) * lo.rec;
+    } else {
+        p->TT = 128;
+        p->stage = lo.scheme == KVQ_SCHEME_INT8 ? 256 * D + 1024 : lo.scheme == KVQ_SCHEME_INT4 ? 128 * D + 1024 : 256 * D;
+    }
+    p->staged = 1;
+    if (tile_bytes(p->N, D) + p->stage > kTreeSmemLimit) {
+        if (p->N >= 64 && tile_bytes(p->N / 2, D) + p->stage <= kTreeSmemLimit) {
+            p->N /= 2;
+        } else if (lo.scheme == KVQ_SCHEME_KIVI) {
+            p->staged = 0;
+            p->stage = 0;
+        } else {
+            return KVQ_ERR_UNSUPPORTED;
+        }
+    }
+    p->RT = (p->rows + p->N - 1) / p->N;
+    const int64_t slots = kMaxTreeBlocks + (int64_t)lo.B * lo.H * p->RT;
+    p->ml_off = 256;
+    p->o_off = align256(p->ml_off + slots * p->N * 8);
+    p->bytes = align256(p->o_off + slots * p->N * D * 4);
     return KVQ_OK;
 }
 
@@ -108,11 +68,10 @@ extern "C" {
 
 int kvq_tree_workspace_bytes(const kvq_config* cfg, int32_t nodes, uint64_t* out_bytes) {
     if (!cfg || !out_bytes) return KVQ_ERR_ARG;
-    kvq::Layout lo;
-    int64_t bytes = 0;
-    const int rc = kvq::tree_plan(cfg, nodes, &lo, &bytes);
+    kvq::TreePlan p;
+    const int rc = kvq::tree_plan(cfg, nodes, &p);
     if (rc != KVQ_OK) return rc;
-    *out_bytes = static_cast<uint64_t>(bytes);
+    *out_bytes = static_cast<uint64_t>(p.bytes);
     return KVQ_OK;
 }
 
@@ -122,12 +81,13 @@ int kvq_tree_attention(const kvq_config* cfg, const void* cache, int32_t layer, 
                        kvq_stream_t stream) {
     if (!cfg || !cache || !q || !k_draft || !v_draft || !out || !workspace) return KVQ_ERR_ARG;
     kvq::TreeArgs a;
-    int64_t bytes = 0;
-    const int rc = kvq::tree_plan(cfg, nodes, &a.lo, &bytes);
+    kvq::TreePlan p;
+    const int rc = kvq::tree_plan(cfg, nodes, &p);
     if (rc != KVQ_OK) return rc;
+    a.lo = p.lo;
     if (layer < 0 || layer >= a.lo.L) return KVQ_ERR_ARG;
     if (a.lo.PG > 0 && a.lo.NG > 0 && !a.lo.table) return KVQ_ERR_ARG;
-    if (workspace_bytes < static_cast<uint64_t>(bytes)) return KVQ_ERR_WORKSPACE;
+    if (workspace_bytes < static_cast<uint64_t>(p.bytes)) return KVQ_ERR_WORKSPACE;
     auto off = [](const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; };
     if (off(cache, 256) || off(workspace, 256) || off(q, 16) || off(k_draft, 16) || off(v_draft, 16) || off(out, 16) ||
         off(n_nodes, 4) || off(a.lo.table, 4))
@@ -140,14 +100,27 @@ int kvq_tree_attention(const kvq_config* cfg, const void* cache, int32_t layer, 
     a.v = static_cast<const __nv_bfloat16*>(v_draft);
     a.mask = mask;
     a.n_nodes = n_nodes;
-    a.scale = softmax_scale * 1.4426950408889634f;
+    a.qscale = softmax_scale * 1.4426950408889634f;
     a.out = static_cast<__nv_bfloat16*>(out);
     a.ws = static_cast<uint8_t*>(workspace);
+    a.rows = p.rows;
+    a.RT = p.RT;
+    a.gshift = a.lo.gqa == 1 ? 0 : a.lo.gqa == 2 ? 1 : a.lo.gqa == 4 ? 2 : 3;
+    a.TT = p.TT;
+    a.staged = p.staged;
+    a.ml_off = p.ml_off;
+    a.o_off = p.o_off;
     if (a.lo.rope_base > 0.0f)
         for (int i = 0; i < a.lo.D / 2; ++i)
             a.rope_w[i] = static_cast<float>(std::pow(static_cast<double>(a.lo.rope_base), -2.0 * i / a.lo.D));
-    kvq::k_tree<<<dim3(nodes, a.lo.Hq, a.lo.B), kvq::kTreeThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
-    return cudaGetLastError() == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    switch (a.lo.D) {
+        case 32: return kvq::launch_tree_d32(a, p.N, p.stage, st);
+        case 64: return kvq::launch_tree_d64(a, p.N, p.stage, st);
+        case 128: return kvq::launch_tree_d128(a, p.N, p.stage, st);
+        case 256: return kvq::launch_tree_d256(a, p.N, p.stage, st);
+        default: return KVQ_ERR_UNSUPPORTED;
+    }
 }
 
 }  // extern "C"

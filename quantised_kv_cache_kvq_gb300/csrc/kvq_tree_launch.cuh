@@ -1,0 +1,26 @@
+// kvq_tree_launch.cuh -- launches one instantiation of the tree attention and of its merge.
+#pragma once
+
+#include "kvq_launch.h"
+#include "kvq_tree.cuh"
+
+namespace kvq {
+
+template <int N, int D>
+int launch_tree_t(TreeArgs& a, int64_t stage, cudaStream_t stream) {
+    const int64_t smem = TreeSmem<N, D>::kStage + stage;
+    int nb = 0;
+    const int rc = decode_blocks(reinterpret_cast<const void*>(k_tree<N, D>), kTreeThreads, smem, &nb);
+    if (rc != KVQ_OK) return rc;
+    a.NB = nb < kMaxTreeBlocks ? nb : kMaxTreeBlocks;
+    if (launch_dependent(k_tree<N, D>, dim3(a.NB), dim3(kTreeThreads), static_cast<size_t>(smem), stream, a) != cudaSuccess)
+        return KVQ_ERR_CUDA;
+    const int64_t units = (int64_t)a.lo.B * a.lo.H * a.RT;
+    constexpr int CW = N < 32 ? N / 2 : 16;
+    return launch_dependent(k_tree_merge<N, D>, dim3(static_cast<unsigned>(units * (N / CW))), dim3(kTreeThreads), 0, stream,
+                            a) == cudaSuccess
+               ? KVQ_OK
+               : KVQ_ERR_CUDA;
+}
+
+}  // namespace kvq
