@@ -11,20 +11,20 @@ namespace {
 
 struct TreePlan {
     Layout lo;
-    int N, RT, rows, TT, staged;
+    int N, RT, rows, TT, stages;
     int64_t stage, ml_off, o_off, bytes;
 };
 
-// Bytes of the operand tiles of k_tree<N, D> (TreeSmem), and what a block may have next to the
-// kernel's static arrays (under 6 KiB).
+// Bytes of the operand tiles of k_tree<N, D> (TreeShape), and what a block may have next to the
+// kernel's static arrays (under 8 KiB).
 int64_t tile_bytes(int N, int D) { return 256 * D + (D > 128 ? 65536 : 32768) + 2 * N * D + 256 * N; }
-constexpr int64_t kTreeSmemLimit = 221 * 1024;
+constexpr int64_t kTreeSmemLimit = 219 * 1024;
 
 // The row tile: the fewest columns, 16 to 128, that hold all queries of a KV head, or 128 (64
-// for heads of 256 channels, whose tiles are twice as large).  The packed bytes of a tile pass
-// through shared memory where they fit next to the operand tiles; with half the columns if
-// that makes the room; else (KIVI records of 256 channels at 8 bits or with outliers) the
-// kernel reads them in place.
+// for heads of 256 channels, whose tiles are twice as large).  The packed bytes of the next two
+// tiles (else the next one) pass through shared memory where they fit next to the operand
+// tiles, with half the columns if that makes the room; else (KIVI records with many outliers,
+// or of 256 channels at 8 bits) the kernel reads them in place.
 int tree_plan(const kvq_config* cfg, int nodes, TreePlan* p) {
     const int rc = make_layout(cfg, cfg->max_tokens, &p->lo);
     if (rc != KVQ_OK) return rc;
@@ -42,16 +42,15 @@ int tree_plan(const kvq_config* cfg, int nodes, TreePlan* p) {
         p->TT = 128;
         p->stage = lo.scheme == KVQ_SCHEME_INT8 ? 256 * D + 1024 : lo.scheme == KVQ_SCHEME_INT4 ? 128 * D + 1024 : 256 * D;
     }
-    p->staged = 1;
-    if (tile_bytes(p->N, D) + p->stage > kTreeSmemLimit) {
-        if (p->N >= 64 && tile_bytes(p->N / 2, D) + p->stage <= kTreeSmemLimit) {
-            p->N /= 2;
-        } else if (lo.scheme == KVQ_SCHEME_KIVI) {
-            p->staged = 0;
-            p->stage = 0;
-        } else {
-            return KVQ_ERR_UNSUPPORTED;
-        }
+    p->stage = (p->stage + 127) / 128 * 128;
+    if (tile_bytes(p->N, D) + p->stage > kTreeSmemLimit && p->N >= 64 &&
+        tile_bytes(p->N / 2, D) + p->stage <= kTreeSmemLimit)
+        p->N /= 2;
+    const int64_t room = kTreeSmemLimit - tile_bytes(p->N, D);
+    p->stages = room >= 2 * p->stage ? 2 : room >= p->stage ? 1 : 0;
+    if (p->stages == 0) {
+        if (lo.scheme != KVQ_SCHEME_KIVI) return KVQ_ERR_UNSUPPORTED;
+        p->stage = 0;
     }
     p->RT = (p->rows + p->N - 1) / p->N;
     const int64_t slots = kMaxTreeBlocks + (int64_t)lo.B * lo.H * p->RT;
@@ -107,7 +106,12 @@ int kvq_tree_attention(const kvq_config* cfg, const void* cache, int32_t layer, 
     a.RT = p.RT;
     a.gshift = a.lo.gqa == 1 ? 0 : a.lo.gqa == 2 ? 1 : a.lo.gqa == 4 ? 2 : 3;
     a.TT = p.TT;
-    a.staged = p.staged;
+    a.TG = a.lo.scheme == KVQ_SCHEME_KIVI ? p.TT / a.lo.G : 0;
+    a.gvshift = 0;
+    while ((1 << a.gvshift) < a.lo.Gv) ++a.gvshift;
+    for (int i = 0; i < 8; ++i) a.group_of[i] = a.TG > 0 && 16 * i < p.TT ? 16 * i / a.lo.G : 0;
+    a.stages = p.stages;
+    a.stage_bytes = static_cast<int>(p.stage);
     a.ml_off = p.ml_off;
     a.o_off = p.o_off;
     if (a.lo.rope_base > 0.0f)
@@ -115,10 +119,10 @@ int kvq_tree_attention(const kvq_config* cfg, const void* cache, int32_t layer, 
             a.rope_w[i] = static_cast<float>(std::pow(static_cast<double>(a.lo.rope_base), -2.0 * i / a.lo.D));
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     switch (a.lo.D) {
-        case 32: return kvq::launch_tree_d32(a, p.N, p.stage, st);
-        case 64: return kvq::launch_tree_d64(a, p.N, p.stage, st);
-        case 128: return kvq::launch_tree_d128(a, p.N, p.stage, st);
-        case 256: return kvq::launch_tree_d256(a, p.N, p.stage, st);
+        case 32: return kvq::launch_tree_d32(a, p.N, st);
+        case 64: return kvq::launch_tree_d64(a, p.N, st);
+        case 128: return kvq::launch_tree_d128(a, p.N, st);
+        case 256: return kvq::launch_tree_d256(a, p.N, st);
         default: return KVQ_ERR_UNSUPPORTED;
     }
 }

@@ -6,8 +6,16 @@
 //   S^T [128 tokens x N]   = K [128 x D] Q^T [D x N]
 //   O^T [D x N]           += V^T [D x 128] P [128 x N]
 // with the tokens (and the channels) on the instruction's M side, so that its cost follows the
-// number of queries, 16 to 128, and a cache byte is dequantised once for all of them.  A
-// thread owns a token (a TMEM lane of S^T) and half of the columns.
+// number of queries, 16 to 128, and a cache byte is dequantised once for all of them.
+//
+// One block per SM, its warps in four roles that hand tiles to each other through mbarriers:
+//   copy      one thread: bulk copies of the packed bytes of the next tiles
+//   unpack    packed bytes -> K and V operand tiles in binary16
+//   product   one thread: issues both products
+//   softmax   scores (TMEM) -> weights P (shared memory), references, sums, results;
+//             a thread owns a token (a TMEM lane of S^T) and some of the columns
+// While the softmax of a tile runs, the next tile's keys are unpacked and its scores computed;
+// its values follow once the weights' product has read the tile's.
 //
 // Softmax, in base 2.  A token's value row is stored in binary16 as v 2^-e (or as its code),
 // v = stored * s; the weight that multiplies it is P = 2^(x + log2 s - m) with a running
@@ -27,7 +35,7 @@
 
 namespace kvq {
 
-constexpr int kTreeThreads = 256;
+constexpr int kMergeThreads = 256;
 constexpr int kMaxTreeBlocks = 608;     // of a launch: bounds the workspace's partial results
 constexpr float kNoMax = -1.0e30f;      // reference of a column that has seen nothing
 constexpr float kHead = 8.0f;           // P of the largest entry, log2
@@ -39,8 +47,10 @@ struct TreeArgs {
     int layer, nodes, rows, RT;         // rows = nodes * gqa, RT row tiles of N columns
     int gshift;                         // log2 gqa
     int NB;                             // blocks of the launch
-    int TT;                             // tokens of a full packed tile
-    int staged;                         // the packed bytes of a tile pass through shared memory
+    int TT, TG;                         // tokens, and groups, of a full packed tile
+    int gvshift;                        // log2 of the value group (it divides a power of two)
+    int group_of[8];                    // KIVI: the group of a tile's 16-token piece
+    int stages, stage_bytes;            // buffers that a tile's packed bytes pass through (0: none)
     const __nv_bfloat16 *q, *k, *v;
     const uint8_t* mask;
     const int32_t* n_nodes;
@@ -74,6 +84,7 @@ __device__ __forceinline__ int64_t tree_head_tiles(const TreeArgs& a, const Tree
 }
 
 // Exclusive place of this thread's value in the block's sum, and the sum.
+template <int NT>
 __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* tmp, int64_t* sum) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int64_t x = v;
@@ -87,7 +98,7 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* tmp, int64_t* 
     __syncthreads();
     int64_t before = 0, all = 0;
 #pragma unroll
-    for (int w = 0; w < kTreeThreads / 32; ++w) {
+    for (int w = 0; w < NT / 32; ++w) {
         if (w < warp) before += tmp[w];
         all += tmp[w];
     }
@@ -96,12 +107,13 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* tmp, int64_t* 
 }
 
 // All tiles of the launch.
+template <int NT>
 __device__ __forceinline__ int64_t tree_total(const TreeArgs& a, int N, int64_t* tmp) {
     int64_t total = 0;
-    for (int b0 = 0; b0 < a.lo.B; b0 += kTreeThreads) {
+    for (int b0 = 0; b0 < a.lo.B; b0 += NT) {
         const int b = b0 + threadIdx.x;
         int64_t sum;
-        block_scan(b < a.lo.B ? a.lo.H * tree_head_tiles(a, tree_seq(a, b, N)) : 0, tmp, &sum);
+        block_scan<NT>(b < a.lo.B ? a.lo.H * tree_head_tiles(a, tree_seq(a, b, N)) : 0, tmp, &sum);
         total += sum;
     }
     return total;
@@ -211,32 +223,37 @@ __device__ __forceinline__ void unit_codes(const uint32_t (&x)[4], uint32_t (&c)
     }
 }
 
-// One packed tile: its groups' records (KIVI), or its rows (the other schemes).
+// One packed tile: its groups' records (KIVI), or its rows (the other schemes).  STAGED: in
+// shared memory, one record after another; else the records are read where they lie.
+template <bool STAGED>
 struct PackedTile {
-    const uint8_t* base;          // staged: the records one after another, or the rows
+    const uint8_t* base;          // STAGED
     int stride;
-    const uint8_t* const* recs;   // not staged: the records' places (base is NULL)
-    const uint8_t* codes[2];      // others: key rows and value rows (FP8: value tiles) of the tile
-    const float* scales[2];       // INT8, INT4
+    const uint8_t* const* recs;   // not STAGED: the records' places
     int cnt;                      // tokens
-    __device__ __forceinline__ const uint8_t* rec(int g) const { return base ? base + g * stride : recs[g]; }
+    int64_t t0;                   // the first one
+    __device__ __forceinline__ const uint8_t* rec(int g) const {
+        if constexpr (STAGED) return base + g * stride;
+        else return recs[g];
+    }
 };
 
-// KIVI keys.  A warp takes 64 channels of 2 D / 64 octets of rows; a lane 16 channels of one row
+// KIVI keys.  A warp takes 64 channels of some octets of rows; a lane 16 channels of one row
 // of each octet, with the group's scales and zeros of its channels in registers.  x = code * s +
 // z is one binary16 fused multiply-add of exact operands: rounded once.
-template <int D, int BITS>
-__device__ __forceinline__ void kivi_keys(const Layout& lo, const PackedTile& t, uint8_t* kt) {
-    constexpr int QUADS = D / 64;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int unit = (warp % QUADS) * 4 + (lane >> 3), o0 = (warp / QUADS) * 2 * QUADS;
+template <int D, int BITS, int DT, typename Tile>
+__device__ __forceinline__ void kivi_keys(const TreeArgs& a, const Tile t, uint8_t* kt, int tid) {
+    constexpr int QUADS = D / 64, PER = 16 * QUADS / (DT / 32);       // octets of a warp
+    const Layout& lo = a.lo;
+    const int warp = tid >> 5, lane = tid & 31;
+    const int unit = (warp % QUADS) * 4 + (lane >> 3), o0 = (warp / QUADS) * PER;
     uint32_t s[8], z[8];
     int have = -1;
 #pragma unroll 2
-    for (int o = o0; o < o0 + 2 * QUADS; ++o) {
+    for (int o = o0; o < o0 + PER; ++o) {
         const int row = 8 * o + (lane & 7), tok = packed_token(row);
         if (8 * (o & ~1) >= t.cnt) break;
-        const int g = (8 * (o & ~1)) / lo.G, tin = tok - g * lo.G;
+        const int g = a.group_of[o >> 1], tin = tok - g * lo.G;
         const uint8_t* rec = t.rec(g);
         if (g != have) {
             have = g;
@@ -270,14 +287,15 @@ __device__ __forceinline__ void kivi_keys(const Layout& lo, const PackedTile& t,
 
 // KIVI values, [channel][token] (K-major): a thread takes one word pair index of two adjacent
 // lanes' codes, four tokens 4 ip .. and their partners 8 later, over 16 / BITS channels.
-template <int D, int BITS>
-__device__ __forceinline__ void kivi_values(const Layout& lo, const PackedTile& t, uint8_t* vt) {
+template <int D, int BITS, int DT, typename Tile>
+__device__ __forceinline__ void kivi_values(const TreeArgs& args, const Tile t, uint8_t* vt, int tid) {
     constexpr int HW = 16 / BITS, WPL = D * BITS / 64, SW = WPL < 4 ? WPL : 4;
-    const int g8 = threadIdx.x & 7, ip = (threadIdx.x >> 3) & 1;
-    for (int it = threadIdx.x >> 4; it < 8 * (WPL / 2); it += kTreeThreads / 16) {
+    const Layout& lo = args.lo;
+    const int g8 = tid & 7, ip = (tid >> 3) & 1;
+    for (int it = tid >> 4; it < 8 * (WPL / 2); it += DT / 16) {
         const int a = it / (WPL / 2), mm = it % (WPL / 2);     // 16-token tile, word pair
         if (16 * a >= t.cnt) break;
-        const int g = 16 * a / lo.G, ti = 16 * a - g * lo.G;   // group, first token in it
+        const int g = args.group_of[a], ti = 16 * a - g * lo.G;   // group, first token in it
         const uint8_t* rec = t.rec(g);
         const int w = 2 * mm;
         const uint8_t* src = rec + lo.kc + 4 * ((ti / 16) * 32 * WPL + (w / SW) * 32 * SW + (4 * g8 + 2 * ip) * SW + w % SW);
@@ -289,7 +307,7 @@ __device__ __forceinline__ void kivi_values(const Layout& lo, const PackedTile& 
 #pragma unroll
         for (int m = 0; m < HW; ++m) {
             const int j = mm * HW + m, c = 16 * (j >> 1) + g8 + 8 * (j & 1);
-            const int gv = c / lo.Gv;
+            const int gv = c >> args.gvshift;
             if (gv != have) {
                 have = gv;
                 s = *reinterpret_cast<const uint4*>(par + 2 * gv * lo.G);
@@ -317,20 +335,21 @@ __device__ __forceinline__ void kivi_values(const Layout& lo, const PackedTile& 
 
 // Largest |value| that the keys (kv = 0) or values of the tile's groups can have, over this
 // thread's share of their parameters; what is not finite is left out.
-__device__ __forceinline__ float kivi_bound(const Layout& lo, const PackedTile& t, int kv) {
+template <int DT, typename Tile>
+__device__ __forceinline__ float kivi_bound(const Layout& lo, const Tile t, int kv, int tid) {
     const float levels = static_cast<float>((1 << lo.bits) - 1);
     const int pairs = kv ? lo.NGv * lo.G : lo.D;
     float top = 0.0f;
     for (int g = 0; g * lo.G < t.cnt; ++g) {
         const __half* par = reinterpret_cast<const __half*>(t.rec(g) + lo.kc + lo.vc + (kv ? lo.kp : 0));
         const uint32_t* side = reinterpret_cast<const uint32_t*>(t.rec(g) + lo.kc + lo.vc + lo.kp + lo.vp + (kv ? lo.ko : 0));
-        for (int i = 2 * threadIdx.x; i < pairs; i += 2 * kTreeThreads) {
+        for (int i = 2 * tid; i < pairs; i += 2 * DT) {
             const float2 s = __half22float2(*reinterpret_cast<const __half2*>(par + i));
             const float2 z = __half22float2(*reinterpret_cast<const __half2*>(par + pairs + i));
             const float x = fmaf(levels, s.x, fabsf(z.x)), y = fmaf(levels, s.y, fabsf(z.y));
             top = fmaxf(top, fmaxf(x < INFINITY ? x : 0.0f, y < INFINITY ? y : 0.0f));
         }
-        for (int i = threadIdx.x; i < lo.K * pairs; i += kTreeThreads) {
+        for (int i = tid; i < lo.K * pairs; i += DT) {
             const float x = fabsf(__uint_as_float(side[i] & 0xffff0000u));
             top = fmaxf(top, x < INFINITY ? x : 0.0f);
         }
@@ -339,9 +358,9 @@ __device__ __forceinline__ float kivi_bound(const Layout& lo, const PackedTile& 
 }
 
 // The same tile where binary16 does not hold its values: element by element, times `scale`.
-template <int D>
-__device__ void kivi_keys_scaled(const Layout& lo, const PackedTile& t, uint8_t* kt, float scale, int W) {
-    for (int i = threadIdx.x; i < 128 * D; i += kTreeThreads) {
+template <int D, int DT, typename Tile>
+__device__ __noinline__ void kivi_keys_scaled(const Layout& lo, const Tile t, uint8_t* kt, float scale, int W, int tid) {
+    for (int i = tid; i < 128 * D; i += DT) {
         const int row = i / D, c = i % D, tok = packed_token(row);
         if (tok >= t.cnt) continue;
         const uint8_t* rec = t.rec(tok / lo.G);
@@ -353,9 +372,9 @@ __device__ void kivi_keys_scaled(const Layout& lo, const PackedTile& t, uint8_t*
         *reinterpret_cast<__half*>(kt + core_at(row, p >> 3, D / 8 * kCoreBytes) + (p & 7) * 2) = __float2half_rn(x * scale);
     }
 }
-template <int D>
-__device__ void kivi_values_scaled(const Layout& lo, const PackedTile& t, uint8_t* vt, float scale) {
-    for (int i = threadIdx.x; i < 128 * D; i += kTreeThreads) {
+template <int D, int DT, typename Tile>
+__device__ __noinline__ void kivi_values_scaled(const Layout& lo, const Tile t, uint8_t* vt, float scale, int tid) {
+    for (int i = tid; i < 128 * D; i += DT) {
         const int tok = i / D, c = i % D;
         if (tok >= t.cnt) continue;
         const uint8_t* rec = t.rec(tok / lo.G);
@@ -368,12 +387,12 @@ __device__ void kivi_values_scaled(const Layout& lo, const PackedTile& t, uint8_
     }
 }
 // The side lists' elements over the dense ones.
-template <int D>
-__device__ void kivi_outliers(const Layout& lo, const PackedTile& t, uint8_t* tile, int kv, float scale, int W) {
+template <int D, int DT, typename Tile>
+__device__ __noinline__ void kivi_outliers(const Layout& lo, const Tile t, uint8_t* tile, int kv, float scale, int W, int tid) {
     const int per = kv ? lo.NGv * lo.G : D;
     for (int g = 0; g * lo.G < t.cnt; ++g) {
         const uint32_t* side = reinterpret_cast<const uint32_t*>(t.rec(g) + lo.kc + lo.vc + lo.kp + lo.vp + (kv ? lo.ko : 0));
-        for (int i = threadIdx.x; i < lo.K * per; i += kTreeThreads) {
+        for (int i = tid; i < lo.K * per; i += DT) {
             const uint32_t e = side[i];
             const int idx = static_cast<int>(e & 0xffffu), at = i % per;
             const __half x = __float2half_rn(__uint_as_float(e & 0xffff0000u) * scale);
@@ -405,33 +424,33 @@ __device__ __forceinline__ void fp8_16(const uint4& v, bool e4m3, uint32_t (&o)[
         o[2 * i + 1] = fp8_pair(w[i] >> 16, e4m3);
     }
 }
-template <int D>
-__device__ __forceinline__ void fp8_keys(const PackedTile& t, bool e4m3, uint8_t* kt) {
+template <int D, int DT>
+__device__ __forceinline__ void fp8_keys(const uint8_t* codes, int cnt, bool e4m3, uint8_t* kt, int tid) {
     constexpr uint32_t sbo = D / 8 * kCoreBytes;
-    for (int i = threadIdx.x; i < 128 * D / 16; i += kTreeThreads) {
+    for (int i = tid; i < 128 * D / 16; i += DT) {
         const int row = (i & 7) + 8 * (i / (D / 2)), unit = (i >> 3) % (D / 16), tok = packed_token(row);
-        if ((row & ~15) >= t.cnt) break;
+        if ((row & ~15) >= cnt) break;
         uint32_t o[8];
-        fp8_16(*reinterpret_cast<const uint4*>(t.codes[0] + tok * D + 16 * unit), e4m3, o);
+        fp8_16(*reinterpret_cast<const uint4*>(codes + tok * D + 16 * unit), e4m3, o);
         *reinterpret_cast<uint4*>(kt + core_at(row, 2 * unit, sbo)) = make_uint4(o[0], o[1], o[2], o[3]);
         *reinterpret_cast<uint4*>(kt + core_at(row, 2 * unit + 1, sbo)) = make_uint4(o[4], o[5], o[6], o[7]);
     }
 }
-template <int D>
-__device__ __forceinline__ void fp8_values(const PackedTile& t, bool e4m3, bool negative, uint8_t* vt) {
-    for (int i = threadIdx.x; i < 8 * D; i += kTreeThreads) {
+template <int D, int DT>
+__device__ __forceinline__ void fp8_values(const uint8_t* codes, int cnt, bool e4m3, bool negative, uint8_t* vt, int tid) {
+    for (int i = tid; i < 8 * D; i += DT) {
         const int c = i % D, a = i / D;
-        if (16 * a >= t.cnt) break;
+        if (16 * a >= cnt) break;
         uint32_t o[8];
-        fp8_16(*reinterpret_cast<const uint4*>(t.codes[1] + (16 * a * D + 16 * c)), e4m3, o);
+        fp8_16(*reinterpret_cast<const uint4*>(codes + (16 * a * D + 16 * c)), e4m3, o);
         if (negative) {                     // the value scale's sign (its size goes to the weights)
 #pragma unroll
             for (int r = 0; r < 8; ++r) o[r] ^= 0x80008000u;
         }
-        if (16 * a + 16 > t.cnt) {          // tokens that the cache does not hold: any bytes
+        if (16 * a + 16 > cnt) {          // tokens that the cache does not hold: any bytes
 #pragma unroll
             for (int r = 0; r < 16; ++r)
-                if (packed_token(16 * a + r) >= t.cnt) o[r / 2] &= r & 1 ? 0x0000ffffu : 0xffff0000u;
+                if (packed_token(16 * a + r) >= cnt) o[r / 2] &= r & 1 ? 0x0000ffffu : 0xffff0000u;
         }
         *reinterpret_cast<uint4*>(vt + core_at(c, 2 * a, 16 * kCoreBytes)) = make_uint4(o[0], o[1], o[2], o[3]);
         *reinterpret_cast<uint4*>(vt + core_at(c, 2 * a + 1, 16 * kCoreBytes)) = make_uint4(o[4], o[5], o[6], o[7]);
@@ -440,15 +459,15 @@ __device__ __forceinline__ void fp8_values(const PackedTile& t, bool e4m3, bool 
 
 // INT8 and INT4 rows: the codes as exact binary16 numbers (the scales go to the scores and the
 // weights); keys K-major, values with their channels inside a row (MN-major).
-template <int D>
-__device__ __forceinline__ void rows_codes(const PackedTile& t, int kv, bool int8, uint8_t* tile) {
-    for (int i = threadIdx.x; i < 128 * D / 16; i += kTreeThreads) {
+template <int D, int DT>
+__device__ __forceinline__ void rows_codes(const uint8_t* codes, int cnt, int kv, bool int8, uint8_t* tile, int tid) {
+    for (int i = tid; i < 128 * D / 16; i += DT) {
         const int row = (i & 7) + 8 * (i / (D / 2)), unit = (i >> 3) % (D / 16);
-        if ((row & ~15) >= t.cnt) break;
+        if ((row & ~15) >= cnt) break;
         uint32_t o[8] = {};
-        if (row < t.cnt) {
+        if (row < cnt) {
             if (int8) {
-                const uint4 v = *reinterpret_cast<const uint4*>(t.codes[kv] + row * D + 16 * unit);
+                const uint4 v = *reinterpret_cast<const uint4*>(codes + row * D + 16 * unit);
                 const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {       // code + 128 as an unsigned byte, less 1152
@@ -457,7 +476,7 @@ __device__ __forceinline__ void rows_codes(const PackedTile& t, int kv, bool int
                     o[2 * j + 1] = hfma2u(((x >> 8) & 0x00ff00ffu) | 0x64006400u, 0x3c003c00u, 0xe480e480u);
                 }
             } else {
-                const uint2 v = *reinterpret_cast<const uint2*>(t.codes[kv] + row * (D / 2) + 8 * unit);
+                const uint2 v = *reinterpret_cast<const uint2*>(codes + row * (D / 2) + 8 * unit);
                 const uint32_t w[2] = {v.x, v.y};
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {       // code + 8 as an unsigned nibble, less 1032
@@ -520,25 +539,28 @@ __device__ __forceinline__ void load_words(const uint16_t* p, uint32_t (&w)[8]) 
     w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w; w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
 }
 
-// bf16 rows (the window's tokens, then the drafts) [r0, r0 + cnt) of unit (b, h): keys, values
-// and their powers of two.  A warp takes an octet of rows, a lane 16 channels of one row at a
-// time; each row is scaled by its own largest element.  *bad: a draft's value is not finite
-// (it is 0 in the tile).
-template <int D>
-__device__ __forceinline__ void raw_rows(const TreeArgs& a, int b, int h, const TreeSeq& s, int r0, int cnt, int W,
+// bf16 rows (the window's tokens, then the drafts) [r0, r0 + cnt) of unit (b, h): the keys
+// (kv = 0) or values into their tile (none: NULL) and their powers of two.  A warp takes an
+// octet of rows, a lane 16 channels of one row at a time; each row is scaled by its own largest
+// element.  *bad: a draft's value is not finite (it is 0 in the tile).
+template <int D, int DT>
+__device__ __noinline__ void raw_rows(const TreeArgs& a, int b, int h, const TreeSeq s, int r0, int cnt, int W,
                                          bool paired_values, uint8_t* kt, uint8_t* vt, float* kf, float* vlog,
-                                         bool* bad) {
+                                         int* bad, int kv, int tid) {
     constexpr int UNITS = D / 16, STEPS = (UNITS + 3) / 4;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = tid >> 5, lane = tid & 31;
     const int window = s.n - s.qn;
-    for (int o = warp; o < 16; o += kTreeThreads / 32) {
+    const uint32_t slot0 = static_cast<uint32_t>(s.qn) % static_cast<uint32_t>(a.lo.C > 0 ? a.lo.C : 1);
+    for (int o = warp; o < 16; o += DT / 32) {
         const int row = 8 * o + (lane & 7), r = r0 + row;
         if ((8 * o & ~15) >= cnt) break;
         const uint16_t *kp = nullptr, *vp = nullptr;
         if (row < cnt) {
             if (r < window) {
-                kp = reinterpret_cast<const uint16_t*>(a.cache + a.lo.ring_off + (unit_index(a.lo, a.layer, b, h) * a.lo.C +
-                                                                                 (s.qn + (int64_t)r) % a.lo.C) * (4 * D));
+                uint32_t slot = slot0 + r;                  // window token r is in slot (qn + r) mod C
+                if (slot >= static_cast<uint32_t>(a.lo.C)) slot -= a.lo.C;
+                kp = reinterpret_cast<const uint16_t*>(a.cache + a.lo.ring_off +
+                                                       (unit_index(a.lo, a.layer, b, h) * a.lo.C + slot) * (4 * D));
                 vp = kp + D;
             } else {
                 const int64_t at = (((int64_t)b * a.nodes + (r - window)) * a.lo.H + h) * D;
@@ -546,8 +568,7 @@ __device__ __forceinline__ void raw_rows(const TreeArgs& a, int b, int h, const 
                 vp = reinterpret_cast<const uint16_t*>(a.v) + at;
             }
         }
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
+        {
             const uint16_t* p = kv ? vp : kp;
             uint32_t w[STEPS][8];
             float top = 0.0f;
@@ -565,11 +586,11 @@ __device__ __forceinline__ void raw_rows(const TreeArgs& a, int b, int h, const 
             const int e = range_exponent(top);
             const float f = pow2i(-e);
             const bool draft = r >= window;
-            if (kv && odd && draft) *bad = true;
+            if (kv && odd && draft) *bad = 1;
 #pragma unroll
             for (int i = 0; i < STEPS; ++i) {
                 const int unit = (lane >> 3) + 4 * i;
-                if (unit >= UNITS) continue;
+                if (unit >= UNITS || !(kv ? vt : kt)) continue;
                 uint32_t hw[8];
                 half_words(w[i], f, kv && draft, hw);
                 if (kv == 0) {
@@ -594,11 +615,11 @@ __device__ __forceinline__ void raw_rows(const TreeArgs& a, int b, int h, const 
 
 // Turns the tile's cached keys by their positions: row r of the tile is token t0 + (its place),
 // rows from `rows` on stay.
-template <int D>
-__device__ void turn_keys(uint8_t* kt, const float* w, int64_t t0, int rows, bool packed_order) {
+template <int D, int DT>
+__device__ __noinline__ void turn_keys(uint8_t* kt, const float* w, int64_t t0, int rows, bool packed_order, int tid) {
     constexpr uint32_t sbo = D / 8 * kCoreBytes;
     constexpr int CH = D / 16;                  // 8-channel chunks of half a row
-    for (int i = threadIdx.x; i < 128 * CH; i += kTreeThreads) {
+    for (int i = tid; i < 128 * CH; i += DT) {
         const int row = (i & 7) + 8 * (i / (8 * CH)), ch = (i >> 3) % CH;
         const int tok = packed_order ? packed_token(row) : row;
         if (tok >= rows) continue;
@@ -622,14 +643,142 @@ __device__ void turn_keys(uint8_t* kt, const float* w, int64_t t0, int rows, boo
     }
 }
 
+// Shapes of an instantiation: N columns, D channels.
 template <int N, int D>
-struct TreeSmem {
-    static constexpr int kVBytes = D > 128 ? 65536 : 32768;     // the product reads 128 channel rows
-    static constexpr int kK = 0, kV = 256 * D, kQ = kV + kVBytes, kP = kQ + 2 * N * D, kStage = kP + 256 * N;
+struct TreeShape {
+    static constexpr int kSoft = N >= 64 ? 8 : 4;               // softmax warps
+    static constexpr int kUnpack = N >= 64 ? 8 : 16;            // unpack warps
+    static constexpr int kThreads = 32 * (kSoft + kUnpack + 2);
+    static constexpr int NH = N / (kSoft / 4);                  // columns of a softmax thread
+    static constexpr bool kKeep = NH <= 32;                     // its scores stay in registers
+    static constexpr int B = kKeep ? NH : 16;                   // columns of one TMEM access
     static constexpr int kDN = D > 128 ? 2 : 1;                 // accumulators of 128 channels
-    static constexpr uint32_t kCols = N * (1 + kDN) <= 32 ? 32 : N * (1 + kDN) <= 64 ? 64 : N * (1 + kDN) <= 128 ? 128
-                                      : N * (1 + kDN) <= 256 ? 256 : 512;
-    static constexpr int kBlocks = N >= 128 || D > 128 ? 1 : 2;
+    static constexpr int kTmem = N * (2 + kDN);                 // two score tiles and O^T
+    static constexpr uint32_t kCols = kTmem <= 64 ? 64 : kTmem <= 128 ? 128 : kTmem <= 256 ? 256 : 512;
+    // shared memory: K, V (the product reads 128 channel rows of it), Q, P, then the stages
+    static constexpr int kVBytes = D > 128 ? 65536 : 32768;
+    static constexpr int kK = 0, kV = 256 * D, kQ = kV + kVBytes, kP = kQ + 2 * N * D, kStage = kP + 256 * N;
+};
+
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+    asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ bool bar_or(int id, int threads, bool p) {
+    uint32_t r;
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, %3, p;\n selp.u32 %0, 1, 0, q;\n}"
+        : "=r"(r)
+        : "r"(static_cast<uint32_t>(p)), "r"(id), "r"(threads)
+        : "memory");
+    return r != 0;
+}
+// Bounded wait by the SM's clock, about a second: the global timer's reads cost more than the
+// hand-over of a tile.
+__device__ __forceinline__ bool mbar_wait_clock(uint64_t* bar, uint32_t parity) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    for (;;) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (clock64() - t0 > 2000000000ll) return false;
+    }
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+// Two binary32 lanes at a time.
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float* x, float* y) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(*x), "=f"(*y) : "l"(v));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// A block's walk over its share of the tiles: segments, each the tiles [first, end) of one row
+// tile of one KV head.  Every role walks on its own.
+struct TreeWalk {
+    int b, h, rt, first, end, unit_tiles;
+    bool live;
+    TreeSeq s;
+    int64_t left;
+    __device__ __forceinline__ void segment() {
+        live = rt < s.live;
+        unit_tiles = live ? s.tiles : 1;
+        end = static_cast<int>(left < unit_tiles - first ? first + left : unit_tiles);
+    }
+    __device__ __forceinline__ void begin(const TreeArgs& a, int N, int b_, int64_t at, int64_t n) {
+        b = b_;
+        left = n;
+        s = tree_seq(a, b, N);
+        const int64_t per = tree_head_tiles(a, s), in = at % per, run = (int64_t)s.live * s.tiles;
+        h = static_cast<int>(at / per);
+        rt = static_cast<int>(in < run ? in / s.tiles : s.live + (in - run));
+        first = static_cast<int>(in < run ? in % s.tiles : 0);
+        segment();
+    }
+    // to the next segment; false at the end of the share
+    __device__ __forceinline__ bool next(const TreeArgs& a, int N) {
+        left -= end - first;
+        if (left <= 0) return false;
+        if (end < unit_tiles) {
+            first = end;
+        } else {
+            first = 0;
+            if (++rt == a.RT) {
+                rt = 0;
+                if (++h == a.lo.H) {
+                    h = 0;
+                    ++b;
+                    s = tree_seq(a, b, N);
+                }
+            }
+        }
+        segment();
+        return true;
+    }
+    __device__ __forceinline__ int packed_count(const TreeArgs& a, int tile) const {
+        const int64_t t0 = (int64_t)tile * a.TT;
+        return static_cast<int>(s.qn - t0 < a.TT ? s.qn - t0 : a.TT);
+    }
+    __device__ __forceinline__ int raw_count(int tile) const {
+        const int all = s.n - s.qn + s.nodes - (tile - s.packed) * 128;
+        return all < 128 ? all : 128;
+    }
+};
+
+// Everything the roles share next to the operand tiles.
+template <int N, int D>
+struct TreeShared {
+    float colg[N], colr[N];         // a column's query scale and minus its reference
+    float fac[N], part[4][N];       // per column: factors; per quadrant: maxima, sums
+    float kf[2][128], vl[2][128];   // a token's score factor and log2 of its value scale
+    float wt[D / 2];                // rotary frequencies in the order of the key tile
+    int64_t scan[32], start[2];
+    uint64_t stage_full[2], stage_empty[2], k_full, k_empty, v_full, pv_done, s_full[2], s_empty[2], p_full, q_full, done;
+    const uint8_t* recs[2][8];
+    uint32_t tmem, top[2];
+    int dead, odd;                  // a wait gave up; a draft's value is not finite
 };
 
 __device__ __forceinline__ float fast_log2(float x) {
@@ -649,518 +798,543 @@ __device__ __forceinline__ float warp_max(float x) {
 }
 
 template <int N, int D>
-__global__ void __launch_bounds__(kTreeThreads, TreeSmem<N, D>::kBlocks) k_tree(const __grid_constant__ TreeArgs a) {
-    using S = TreeSmem<N, D>;
-    constexpr int NH = N / 2;                       // columns of a thread
-    constexpr int STEP = NH < 32 ? NH : 32;         // columns of one TMEM access
+__global__ void __launch_bounds__(TreeShape<N, D>::kThreads, 1) k_tree(const __grid_constant__ TreeArgs a) {
+    using S = TreeShape<N, D>;
+    constexpr int NT = S::kThreads, ST = 32 * S::kSoft, DT = 32 * S::kUnpack;
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ __align__(16) float2 col[N];         // (query scale, -reference) of a column
-    __shared__ float fac[N], cmax[4][N], lsum[4][N], kf[128], vlog[128], wt[D / 2];
-    __shared__ int64_t scan[8], start[4];
-    __shared__ uint64_t bar_stage, bar_s, bar_pv;
-    __shared__ uint32_t tmem_slot, top[2];
-    __shared__ const uint8_t* recs[8];
-    __shared__ int dead;
+    __shared__ __align__(16) TreeShared<N, D> sh;
 
     const Layout& lo = a.lo;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = warp & 3, half = warp >> 2;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int H = lo.H, gqa = lo.gqa, W = key_block(lo);
     uint8_t *kt = smem + S::kK, *vt = smem + S::kV, *qt = smem + S::kQ, *pt = smem + S::kP, *stage = smem + S::kStage;
     const bool kivi = lo.scheme == KVQ_SCHEME_KIVI, fp8 = is_fp8(lo.scheme), rows_scheme = is_rows(lo.scheme);
     const bool rope = lo.rope_base > 0.0f;
-    const int64_t row_bytes = lo.scheme == KVQ_SCHEME_INT4 ? D / 2 : D;     // of a code row
+    const int row_bytes = lo.scheme == KVQ_SCHEME_INT4 ? D / 2 : D;     // of a code row
 
+    if (warp == 0) tmem_alloc(&sh.tmem, S::kCols);
+    if (tid == 32) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.stage_full[i], 1);
+            mbar_init(&sh.stage_empty[i], S::kUnpack);
+            mbar_init(&sh.s_full[i], 2);
+            mbar_init(&sh.s_empty[i], S::kSoft);
+        }
+        mbar_init(&sh.k_full, S::kUnpack);
+        mbar_init(&sh.k_empty, 1);
+        mbar_init(&sh.v_full, S::kUnpack);
+        mbar_init(&sh.pv_done, 1);
+        mbar_init(&sh.p_full, S::kSoft);
+        mbar_init(&sh.q_full, S::kSoft);
+        mbar_init(&sh.done, 1);
+        sh.dead = 0;
+        sh.odd = 0;
+    }
+    if (rope)
+        for (int i = tid; i < D / 2; i += NT) sh.wt[i] = a.rope_w[place_channel(i, W, D)];
     grid_dependency_wait();
     grid_launch_dependents();
     // this block's tiles: positions [x0, x1) of all tiles, in the order sequence, KV head, row
     // tile, tile
-    const int64_t total = tree_total(a, N, scan);
+    const int64_t total = tree_total<NT>(a, N, sh.scan);
     const int64_t nb = total < a.NB ? total : a.NB;     // blocks with a share
-    if (blockIdx.x >= nb) return;
     const int64_t x0 = total * blockIdx.x / nb, x1 = total * (blockIdx.x + 1) / nb;
     {
         int64_t base = 0;
-        for (int b0 = 0; b0 < lo.B; b0 += kTreeThreads) {
+        for (int b0 = 0; b0 < lo.B; b0 += NT) {
             const int b = b0 + tid;
             const int64_t w = b < lo.B ? H * tree_head_tiles(a, tree_seq(a, b, N)) : 0;
             int64_t sum;
-            const int64_t at = base + block_scan(w, scan, &sum);
+            const int64_t at = base + block_scan<NT>(w, sh.scan, &sum);
             if (at <= x0 && x0 < at + w) {
-                start[0] = b;
-                start[1] = x0 - at;
+                sh.start[0] = b;
+                sh.start[1] = x0 - at;
             }
             base += sum;
         }
     }
-    if (warp == 0) tmem_alloc(&tmem_slot, S::kCols);
-    if (tid == 32) {
-        mbar_init(&bar_stage, 1);
-        mbar_init(&bar_s, 1);
-        mbar_init(&bar_pv, 1);
-        dead = 0;
-    }
-    if (rope)
-        for (int i = tid; i < D / 2; i += kTreeThreads) wt[i] = a.rope_w[place_channel(i, W, D)];
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
-    const uint32_t tm_s = tmem_slot, tm_o = tm_s + N;
-    const uint32_t my_s = tm_s + (static_cast<uint32_t>(32 * quad) << 16) + half * NH;
+    const uint32_t tm_s = sh.tmem, tm_o = tm_s + 2 * N;
 
+    auto dead = [&]() { return *static_cast<volatile int*>(&sh.dead) != 0; };
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (*static_cast<volatile int*>(&dead)) return;
-        if (!mbar_wait_bounded(bar, parity, kWaitLimitNs)) {
-            dead = 1;
+        if (dead()) return;
+        if (!mbar_wait_clock(bar, parity & 1)) {
+            sh.dead = 1;
             atomicOr(reinterpret_cast<uint32_t*>(a.ws), KVQ_STATUS_TIMEOUT);
         }
     };
-    // tile `tile` of (b, h) brought to the stage: thread 0
-    auto issue = [&](int b, int h, int tile, int qn) {
-        const int64_t t0 = (int64_t)tile * a.TT;
-        const int cnt = static_cast<int>(qn - t0 < a.TT ? qn - t0 : a.TT);
-        if (kivi) {
-            const int ng = cnt / lo.G;
-            mbar_arrive_expect_tx(&bar_stage, static_cast<uint32_t>(ng * lo.rec));
-            if (lo.PG == 0) {
-                bulk_copy_g2s(stage, a.cache + group_offset(lo, a.layer, b, h, t0 / lo.G), ng * lo.rec, &bar_stage);
-            } else {
-                for (int g = 0; g < ng; ++g) {
-                    int64_t off = group_offset(lo, a.layer, b, h, t0 / lo.G + g);
-                    if (off < 0) {      // a table entry outside the pool: page 0 in its place, reported
-                        atomicOr(reinterpret_cast<uint32_t*>(a.ws), KVQ_STATUS_BAD_PAGE);
-                        off = lo.data_off + (((int64_t)a.layer * H + h) * lo.PG + (t0 / lo.G + g) % lo.PG) * lo.rec;
-                    }
-                    bulk_copy_g2s(stage + g * lo.rec, a.cache + off, lo.rec, &bar_stage);
-                }
-            }
-        } else {
-            const int c16 = (cnt + 15) & ~15;
-            const uint8_t* base = a.cache + lo.data_off + unit_index(lo, a.layer, b, h) * lo.unit;
-            const uint32_t bytes = static_cast<uint32_t>(c16 * row_bytes);
-            mbar_arrive_expect_tx(&bar_stage, 2 * bytes + (rows_scheme ? 8 * c16 : 0));
-            bulk_copy_g2s(stage, base + t0 * row_bytes, bytes, &bar_stage);
-            bulk_copy_g2s(stage + 128 * row_bytes, base + (lo.T16 + t0) * row_bytes, bytes, &bar_stage);
-            if (rows_scheme) {
-                const uint8_t* sc = base + 2 * (int64_t)lo.T16 * row_bytes;
-                bulk_copy_g2s(stage + 256 * row_bytes, sc + 4 * t0, 4 * c16, &bar_stage);
-                bulk_copy_g2s(stage + 256 * row_bytes + 512, sc + 4 * (lo.T16 + t0), 4 * c16, &bar_stage);
-            }
-        }
+    // a warp's shared-memory writes, ready for the products
+    auto publish = [&](uint64_t* bar) {
+        smem_to_async();
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
     };
 
-    int b = static_cast<int>(start[0]), h, rt, tile;
-    TreeSeq s = tree_seq(a, b, N);
-    {
-        const int64_t per = tree_head_tiles(a, s), in = start[1] % per;
-        h = static_cast<int>(start[1] / per);
-        if (in < (int64_t)s.live * s.tiles) {
-            rt = static_cast<int>(in / s.tiles);
-            tile = static_cast<int>(in % s.tiles);
-        } else {
-            rt = static_cast<int>(s.live + (in - (int64_t)s.live * s.tiles));
-            tile = 0;
-        }
-    }
-    uint32_t ph_stage = 0, ph_s = 0, ph_pv = 0;
-    bool fetched = false;                       // the current tile is on its way to the stage
-    bool pv_open = false;                       // a value product has not been waited for
-    int64_t left = x1 - x0;
-
-    while (left > 0) {
-        // ------------------------------------------------------------ a segment: tiles [tile, end)
-        const bool live = rt < s.live;
-        const int unit_tiles = live ? s.tiles : 1;
-        const int first = tile;
-        const int end = static_cast<int>(left < unit_tiles - tile ? tile + left : unit_tiles);
-        if (live && !fetched && first < s.packed && a.staged) {
-            if (tid == 0) issue(b, h, first, s.qn);
-            fetched = true;
-        }
-        const int row0 = rt * N, row_end = s.nodes << a.gshift;
-        bool nonfinite = false;
-        float l[NH];
+    if (static_cast<int64_t>(blockIdx.x) < nb) {
+        TreeWalk w;
+        w.begin(a, N, static_cast<int>(sh.start[0]), sh.start[1], x1 - x0);
+        if (warp < S::kSoft) {
+            // ======================================================================= softmax
+            const int quad = warp & 3, half = warp >> 2, row = 32 * quad + lane, col0 = half * S::NH;
+            const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
+            uint32_t it = 0;
+            do {
+                const int row0 = w.rt * N, row_end = w.s.nodes << a.gshift;
+                float l[S::NH];
 #pragma unroll
-        for (int i = 0; i < NH; ++i) l[i] = 0.0f;
-        if (live) {
-            // queries: a warp takes an octet of columns, a lane 16 channels at a time
-            constexpr int UNITS = D / 16, STEPS = (UNITS + 3) / 4;
-            for (int o = warp; o < N / 8; o += kTreeThreads / 32) {
-                const int c = 8 * o + (lane & 7), r = row0 + c;
-                const uint16_t* p = nullptr;
-                if (r < row_end)
-                    p = reinterpret_cast<const uint16_t*>(a.q) +
-                        (((int64_t)b * a.nodes + (r >> a.gshift)) * lo.Hq + h * gqa + (r & (gqa - 1))) * D;
-                uint32_t w[STEPS][8];
-                float mx = 0.0f;
-                bool odd = false;
+                for (int i = 0; i < S::NH; ++i) l[i] = 0.0f;
+                if (w.live) {
+                    // queries: a warp takes an octet of columns, a lane 16 channels at a time
+                    constexpr int UNITS = D / 16, STEPS = (UNITS + 3) / 4;
+                    for (int o = warp; o < N / 8; o += S::kSoft) {
+                        const int c = 8 * o + (lane & 7), r = row0 + c;
+                        const uint16_t* p = nullptr;
+                        if (r < row_end)
+                            p = reinterpret_cast<const uint16_t*>(a.q) +
+                                (((int64_t)w.b * a.nodes + (r >> a.gshift)) * lo.Hq + w.h * gqa + (r & (gqa - 1))) * D;
+                        uint32_t q[STEPS][8];
+                        float mx = 0.0f;
+                        bool odd = false;
 #pragma unroll
-                for (int i = 0; i < STEPS; ++i) {
-                    const int unit = (lane >> 3) + 4 * i;
+                        for (int i = 0; i < STEPS; ++i) {
+                            const int unit = (lane >> 3) + 4 * i;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) w[i][j] = 0u;
-                    if (p && unit < UNITS) load_words(p + 16 * unit, w[i]);
-                    mx = fmaxf(mx, unit_top(w[i], &odd));
-                }
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                const int e = range_exponent(mx);
-                const float f = pow2i(-e);
-#pragma unroll
-                for (int i = 0; i < STEPS; ++i) {
-                    const int unit = (lane >> 3) + 4 * i;
-                    if (unit >= UNITS) continue;
-                    uint32_t hw[8];
-                    half_words(w[i], f, false, hw);
-                    store_unit<D>(qt, c, unit, hw, W);
-                }
-                if (lane < 8) col[c] = make_float2(a.qscale * pow2i(e), -kNoMax);
-            }
-        }
-
-        // ------------------------------------------------------------ tiles
-        bool have_o = false;                    // O^T holds this segment's sum
-        for (; tile < end; ++tile) {
-            if (!live) continue;
-            const bool packed = tile < s.packed;
-            const int r0 = (tile - s.packed) * 128;                     // of the raw rows
-            int cnt;
-            PackedTile t;
-            t.stride = lo.rec;
-            t.recs = recs;
-            if (packed) {
-                const int64_t t0 = (int64_t)tile * a.TT;
-                cnt = static_cast<int>(s.qn - t0 < a.TT ? s.qn - t0 : a.TT);
-                if (a.staged) {
-                    wait(&bar_stage, ph_stage);
-                    ph_stage ^= 1;
-                    fetched = false;
-                    t.base = stage;
-                    t.codes[0] = stage;
-                    t.codes[1] = stage + 128 * row_bytes;
-                    t.scales[0] = reinterpret_cast<const float*>(stage + 256 * row_bytes);
-                    t.scales[1] = t.scales[0] + 128;
-                } else {
-                    // records too large to pass through shared memory next to the tiles
-                    if (tid < 8 && tid * lo.G < cnt) {
-                        int64_t off = group_offset(lo, a.layer, b, h, t0 / lo.G + tid);
-                        if (off < 0) {
-                            atomicOr(reinterpret_cast<uint32_t*>(a.ws), KVQ_STATUS_BAD_PAGE);
-                            off = lo.data_off + (((int64_t)a.layer * H + h) * lo.PG + (t0 / lo.G + tid) % lo.PG) * lo.rec;
+                            for (int j = 0; j < 8; ++j) q[i][j] = 0u;
+                            if (p && unit < UNITS) load_words(p + 16 * unit, q[i]);
+                            mx = fmaxf(mx, unit_top(q[i], &odd));
                         }
-                        recs[tid] = a.cache + off;
-                    }
-                    __syncthreads();
-                    t.base = nullptr;
-                }
-                t.cnt = cnt;
-            } else {
-                const int all = s.n - s.qn + s.nodes - r0;
-                cnt = all < 128 ? all : 128;
-            }
-            const int steps = (cnt + 15) >> 4;                         // of 16 tokens
-            float kscale = 1.0f, vscale = 1.0f;                        // KIVI: stored = value * scale
-            int ke = 0, ve = 0;
-            if (packed && kivi) {
-                if (tid < 2) top[tid] = 0u;
-                __syncthreads();
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                        const int e = range_exponent(mx);
+                        const float f = pow2i(-e);
 #pragma unroll
-                for (int kv = 0; kv < 2; ++kv) {
-                    const float m = warp_max(kivi_bound(lo, t, kv));
-                    if (lane == 0) atomicMax(&top[kv], __float_as_uint(m));
+                        for (int i = 0; i < STEPS; ++i) {
+                            const int unit = (lane >> 3) + 4 * i;
+                            if (unit >= UNITS) continue;
+                            uint32_t hw[8];
+                            half_words(q[i], f, false, hw);
+                            store_unit<D>(qt, c, unit, hw, W);
+                        }
+                        if (lane < 8) {
+                            sh.colg[c] = a.qscale * pow2i(e);
+                            sh.colr[c] = -kNoMax;
+                        }
+                    }
+                    publish(&sh.q_full);
+                    bar_sync(2, ST);
                 }
-                __syncthreads();
-                const float kb = __uint_as_float(top[0]), vb = __uint_as_float(top[1]);
-                if (kb >= 32768.0f) {
-                    ke = range_exponent(kb);
-                    kscale = pow2i(-ke);
+                const int first = w.first;
+                for (int tile = first; w.live && tile < w.end; ++tile, ++it) {
+                    const bool packed = tile < w.s.packed;
+                    const int cnt = packed ? w.packed_count(a, tile) : w.raw_count(tile);
+                    const int tok = packed && !rows_scheme ? packed_token(row) : row;
+                    const bool valid = tok < cnt, masked = cnt < 128 || !packed;
+                    int draft = -1;
+                    if (!packed && valid) draft = (tile - w.s.packed) * 128 + row - (w.s.n - w.s.qn);
+                    const uint32_t my_s = tm_s + (it & 1) * N + lanes + col0;
+                    wait(&sh.s_full[it & 1], it >> 1);
+                    tmem_fence_after();
+                    const float f = valid ? sh.kf[it & 1][row] : 0.0f, lv = valid ? sh.vl[it & 1][row] : 0.0f;
+                    const float inv = tree_exp2(-lv);
+                    const uint64_t f2 = pack2(f, f), lv2 = pack2(lv, lv), inv2 = pack2(inv, inv);
+                    // x + log2 s of B columns from c0 on, less the references if REF
+                    auto scores = [&](int c0, float (&x)[S::B], bool ref) {
+                        tmem_load(my_s + c0, x);
+#pragma unroll
+                        for (int i = 0; i < S::B; i += 4) {
+                            const ulonglong2 g = *reinterpret_cast<const ulonglong2*>(&sh.colg[col0 + c0 + i]);
+                            uint64_t u = fma2(pack2(x[i], x[i + 1]), mul2(f2, g.x), lv2);
+                            uint64_t v = fma2(pack2(x[i + 2], x[i + 3]), mul2(f2, g.y), lv2);
+                            if (ref) {
+                                const ulonglong2 r = *reinterpret_cast<const ulonglong2*>(&sh.colr[col0 + c0 + i]);
+                                u = add2(u, r.x);
+                                v = add2(v, r.y);
+                            }
+                            unpack2(u, &x[i], &x[i + 1]);
+                            unpack2(v, &x[i + 2], &x[i + 3]);
+                        }
+                        if (masked) {
+#pragma unroll
+                            for (int i = 0; i < S::B; ++i) {
+                                bool see = valid;
+                                if (draft >= 0) {
+                                    const int r = row0 + col0 + c0 + i, node = r >> a.gshift;
+                                    see = r < row_end && (a.mask ? a.mask[((int64_t)w.b * a.nodes + node) * a.nodes + draft] != 0
+                                                                 : draft <= node);
+                                }
+                                x[i] = see ? x[i] : -INFINITY;
+                            }
+                        }
+                    };
+                    float x[S::B];
+                    float hi = kNoMax;
+#pragma unroll
+                    for (int c0 = 0; c0 < S::NH; c0 += S::B) {
+                        scores(c0, x, true);
+#pragma unroll
+                        for (int i = 0; i < S::B; i += 2) hi = max3(hi, x[i], x[i + 1]);
+                    }
+                    const bool over = bar_or(2, ST, hi > kReach);
+                    if (over) {
+                        // the columns' maxima over the tile, the new references, and everything so
+                        // far under them
+#pragma unroll 1
+                        for (int c0 = 0; c0 < S::NH; c0 += S::B) {
+                            scores(c0, x, false);
+#pragma unroll
+                            for (int i = 0; i < S::B; ++i) {
+                                const float m = warp_max(x[i]);
+                                if (lane == 0) sh.part[quad][col0 + c0 + i] = m;
+                            }
+                        }
+                        bar_sync(2, ST);
+                        for (int c = tid; c < N; c += ST) {
+                            const float m = fmaxf(fmaxf(sh.part[0][c], sh.part[1][c]), fmaxf(sh.part[2][c], sh.part[3][c])) - kHead;
+                            const float old = -sh.colr[c], now = fmaxf(old, m);
+                            sh.colr[c] = -now;
+                            sh.fac[c] = tree_exp2(old - now);
+                        }
+                        bar_sync(2, ST);
+                        if (S::kKeep) scores(0, x, true);
+                    }
+                    if (S::kKeep) {                     // the scores are out of TMEM
+                        tmem_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sh.s_empty[it & 1]);
+                    }
+                    wait(&sh.pv_done, it + 1);          // of the tile before: P is free, O^T at rest
+                    tmem_fence_after();
+                    if (over && tile > first) {
+#pragma unroll
+                        for (int i = 0; i < S::NH; ++i) l[i] *= sh.fac[col0 + i];
+#pragma unroll 1
+                        for (int d = 0; d < S::kDN; ++d)
+#pragma unroll 1
+                            for (int c0 = 0; c0 < S::NH; c0 += 8) {
+                                float o[8];
+                                const uint32_t at = tm_o + d * N + lanes + col0 + c0;
+                                tmem_load(at, o);
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) o[i] *= sh.fac[col0 + c0 + i];
+                                tmem_store(at, o);
+                            }
+                    }
+                    uint8_t* prow = pt + (row >> 3) * kCoreBytes + (row & 7) * 16;
+#pragma unroll
+                    for (int c0 = 0; c0 < S::NH; c0 += S::B) {
+                        if (!S::kKeep) scores(c0, x, true);
+#pragma unroll
+                        for (int c = 0; c < S::B; c += 8) {
+                            uint32_t p[4];
+#pragma unroll
+                            for (int i = 0; i < 8; i += 2) {
+                                const float p0 = tree_exp2(x[c + i]), p1 = tree_exp2(x[c + i + 1]);
+                                float& l0 = l[c0 + c + i];
+                                float& l1 = l[c0 + c + i + 1];
+                                unpack2(fma2(pack2(p0, p1), inv2, pack2(l0, l1)), &l0, &l1);
+                                p[i / 2] = h2_as_u32(__floats2half2_rn(p0, p1));
+                            }
+                            *reinterpret_cast<uint4*>(prow + ((col0 + c0 + c) >> 3) * (16 * kCoreBytes)) =
+                                make_uint4(p[0], p[1], p[2], p[3]);
+                        }
+                    }
+                    if (!S::kKeep) {
+                        tmem_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sh.s_empty[it & 1]);
+                    }
+                    publish(&sh.p_full);
                 }
-                if (vb >= 32768.0f) {
-                    ve = range_exponent(vb);
-                    vscale = pow2i(-ve);
+                // ------------------------------------------------------ the segment's result
+                const bool whole = first == 0 && w.end == w.unit_tiles;
+                const int64_t unit = ((int64_t)w.b * H + w.h) * a.RT + w.rt;
+                const int64_t slot = blockIdx.x + unit;
+                if (w.live) wait(&sh.pv_done, it + 1);
+                tmem_fence_after();
+                // the sums over a column's tokens
+#pragma unroll
+                for (int i = 0; i < S::NH; ++i) {
+                    float v = l[i];
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+                    if (lane == 0) sh.part[quad][col0 + i] = v;
                 }
-            }
-            // ---- keys (the previous tile's score product is done: its scores were read)
-            if (!packed) {
-                if (pv_open) {                                          // the rows write both tiles
-                    wait(&bar_pv, ph_pv);
-                    ph_pv ^= 1;
-                    pv_open = false;
+                bar_sync(2, ST);
+                for (int c = tid; c < N; c += ST) {
+                    // rows of padding nodes saw the cached tokens with a query of 0: their output is 0
+                    const float v = w.live && row0 + c < row_end
+                                        ? (sh.part[0][c] + sh.part[1][c]) + (sh.part[2][c] + sh.part[3][c])
+                                        : 0.0f;
+                    if (whole) {
+                        sh.fac[c] = v != 0.0f ? 1.0f / v : 0.0f;
+                    } else {
+                        sh.fac[c] = v != 0.0f ? 1.0f : 0.0f;
+                        reinterpret_cast<float2*>(a.ws + a.ml_off)[slot * N + c] = make_float2(-sh.colr[c], v);
+                    }
                 }
-                raw_rows<D>(a, b, h, s, r0, cnt, W, rows_scheme, kt, vt, kf, vlog, &nonfinite);
-            } else if (kivi) {
-                if (kscale != 1.0f)
-                    kivi_keys_scaled<D>(lo, t, kt, kscale, W);
+                bar_sync(2, ST);
+                const bool odd = sh.odd != 0;
+#pragma unroll 1
+                for (int d = 0; d < S::kDN; ++d) {
+                    const int ch0 = 128 * d + 32 * quad;
+                    if (ch0 >= D) continue;
+                    // lane -> channel: the order of the tile's value rows
+                    const int ch = rows_scheme ? place_channel(ch0 + lane, W, D) : ch0 + lane;
+#pragma unroll 1
+                    for (int c0 = 0; c0 < S::NH; c0 += 8) {
+                        float o[8];
+                        if (w.live) tmem_load(tm_o + d * N + lanes + col0 + c0, o);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int c = col0 + c0 + i, r = row0 + c;
+                            if (r >= a.rows) continue;
+                            const float fc = sh.fac[c];
+                            float v = fc != 0.0f ? o[i] * fc : 0.0f;
+                            if (odd && r < row_end) {   // drafts whose value is not finite, in the rows that see them
+                                const int node = r >> a.gshift;
+                                for (int j = 0; j < w.s.nodes; ++j) {
+                                    const float y = __bfloat162float(a.v[(((int64_t)w.b * a.nodes + j) * H + w.h) * D + ch]);
+                                    if (fabsf(y) < INFINITY) continue;
+                                    if (a.mask ? a.mask[((int64_t)w.b * a.nodes + node) * a.nodes + j] != 0 : j <= node) v += y;
+                                }
+                            }
+                            if (whole)
+                                a.out[(((int64_t)w.b * a.nodes + (r >> a.gshift)) * lo.Hq + w.h * gqa + (r & (gqa - 1))) * D + ch] =
+                                    __float2bfloat16_rn(v);
+                            else
+                                reinterpret_cast<float*>(a.ws + a.o_off)[(slot * N + c) * D + ch] = v;
+                        }
+                    }
+                }
+                tmem_fence_before();
+                bar_sync(2, ST);
+            } while (w.next(a, N));
+        } else if (warp < S::kSoft + S::kUnpack) {
+            // ======================================================================== unpack
+            const int ut = tid - ST;
+            uint32_t it = 0, staged = 0;
+            // one packed KIVI tile, from wherever its records lie
+            auto kivi_tile = [&](const auto& t, uint64_t* empty) {
+                const bool big = bar_or(1, DT, kivi_bound<DT>(lo, t, 0, ut) >= 32768.0f || kivi_bound<DT>(lo, t, 1, ut) >= 32768.0f);
+                int ke = 0, ve = 0;
+                if (big) {      // outside binary16: the tile's keys or values under a power of two
+                    if (ut < 2) sh.top[ut] = 0u;
+                    bar_sync(1, DT);
+                    for (int kv = 0; kv < 2; ++kv)
+                        atomicMax(&sh.top[kv], __float_as_uint(kivi_bound<DT>(lo, t, kv, ut)));
+                    bar_sync(1, DT);
+                    if (__uint_as_float(sh.top[0]) >= 32768.0f) ke = range_exponent(__uint_as_float(sh.top[0]));
+                    if (__uint_as_float(sh.top[1]) >= 32768.0f) ve = range_exponent(__uint_as_float(sh.top[1]));
+                }
+                if (ut < 128) {
+                    sh.kf[it & 1][ut] = pow2i(ke);
+                    sh.vl[it & 1][ut] = static_cast<float>(ve);
+                }
+                wait(&sh.k_empty, it + 1);
+                if (ke != 0)
+                    kivi_keys_scaled<D, DT>(lo, t, kt, pow2i(-ke), W, ut);
                 else if constexpr (D >= 64) {
-                    if (lo.bits == 2) kivi_keys<D, 2>(lo, t, kt);
-                    else if (lo.bits == 4) kivi_keys<D, 4>(lo, t, kt);
-                    else kivi_keys<D, 8>(lo, t, kt);
+                    if (lo.bits == 2) kivi_keys<D, 2, DT>(a, t, kt, ut);
+                    else if (lo.bits == 4) kivi_keys<D, 4, DT>(a, t, kt, ut);
+                    else kivi_keys<D, 8, DT>(a, t, kt, ut);
                 }
                 if (lo.K > 0) {
-                    __syncthreads();
-                    kivi_outliers<D>(lo, t, kt, 0, kscale, W);
+                    bar_sync(1, DT);
+                    kivi_outliers<D, DT>(lo, t, kt, 0, pow2i(-ke), W, ut);
                 }
-            } else if (fp8) {
-                fp8_keys<D>(t, lo.scheme == KVQ_SCHEME_FP8_E4M3, kt);
-            } else {
-                rows_codes<D>(t, 0, lo.scheme == KVQ_SCHEME_INT8, kt);
-            }
-            if (rope) {
-                __syncthreads();
-                if (packed)
-                    turn_keys<D>(kt, wt, (int64_t)tile * a.TT, cnt, true);
-                else
-                    turn_keys<D>(kt, wt, (int64_t)s.qn + r0, s.n - s.qn - r0 < cnt ? s.n - s.qn - r0 : cnt, false);
-            }
-            smem_to_async();
-            tmem_fence_before();
-            __syncthreads();
-            if (tid == 0) {
-                tmem_fence_after();
-                const uint64_t da = mma_desc(smem_addr(kt), D / 8 * kCoreBytes), db = mma_desc(smem_addr(qt), D / 8 * kCoreBytes);
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-                    mma_f16(tm_s, da + k * (2 * kCoreBytes >> 4), db + k * (2 * kCoreBytes >> 4),
-                            mma_idesc(128, N, false, false), k > 0);
-                mma_commit(&bar_s);
-            }
-            // ---- values, while the scores are computed
-            if (pv_open) {
-                wait(&bar_pv, ph_pv);
-                ph_pv ^= 1;
-                pv_open = false;
-            }
-            if (packed) {
-                if (kivi) {
-                    if (vscale != 1.0f)
-                        kivi_values_scaled<D>(lo, t, vt, vscale);
-                    else if constexpr (D >= 64) {
-                        if (lo.bits == 2) kivi_values<D, 2>(lo, t, vt);
-                        else if (lo.bits == 4) kivi_values<D, 4>(lo, t, vt);
-                        else kivi_values<D, 8>(lo, t, vt);
-                    }
-                    if (lo.K > 0) {
-                        __syncthreads();
-                        kivi_outliers<D>(lo, t, vt, 1, vscale, W);
-                    }
-                } else if (fp8) {
-                    fp8_values<D>(t, lo.scheme == KVQ_SCHEME_FP8_E4M3, fp8_scale(a, h)[1] < 0.0f, vt);
-                } else {
-                    rows_codes<D>(t, 1, lo.scheme == KVQ_SCHEME_INT8, vt);
+                if (rope) {
+                    bar_sync(1, DT);
+                    turn_keys<D, DT>(kt, sh.wt, t.t0, t.cnt, true, ut);
                 }
-            }
-            // ---- this thread's token: factor of its scores, log2 of its values' scale
-            const int row = 32 * quad + lane;
-            const int tok = packed && (kivi || fp8) ? packed_token(row) : row;
-            const bool valid = tok < cnt;
-            float f = 0.0f, lv = 0.0f;
-            int draft = -1;
-            if (valid) {
-                if (!packed) {
-                    f = kf[row];
-                    lv = vlog[row];
-                    draft = r0 + row - (s.n - s.qn);
-                } else if (kivi) {
-                    f = pow2i(ke);
-                    lv = static_cast<float>(ve);
-                } else if (fp8) {
-                    const float* sc = fp8_scale(a, h);
-                    f = sc[0];
-                    lv = fast_log2(fabsf(sc[1]));
-                } else {
-                    f = t.scales[0][tok];
-                    lv = fast_log2(t.scales[1][tok]);
+                publish(&sh.k_full);
+                wait(&sh.pv_done, it + 1);
+                if (ve != 0)
+                    kivi_values_scaled<D, DT>(lo, t, vt, pow2i(-ve), ut);
+                else if constexpr (D >= 64) {
+                    if (lo.bits == 2) kivi_values<D, 2, DT>(a, t, vt, ut);
+                    else if (lo.bits == 4) kivi_values<D, 4, DT>(a, t, vt, ut);
+                    else kivi_values<D, 8, DT>(a, t, vt, ut);
                 }
-                lv = fmaxf(lv, -110.0f);        // (a scale of 0 belongs to codes of 0)
-            }
-            const float inv = tree_exp2(-lv);
-            __syncthreads();                    // the stage is read: the next tile may come
-            {
-                // the next packed tile of this block, in this segment (the next segment's first
-                // tile is fetched when it begins)
-                if (a.staged && tile + 1 < end && tile + 1 < s.packed) {
-                    if (tid == 0) issue(b, h, tile + 1, s.qn);
-                    fetched = true;
+                if (lo.K > 0) {
+                    bar_sync(1, DT);
+                    kivi_outliers<D, DT>(lo, t, vt, 1, pow2i(-ve), W, ut);
                 }
-            }
-            wait(&bar_s, ph_s);
-            ph_s ^= 1;
-            tmem_fence_after();
-            // ---- softmax
-            float x[NH];
-#pragma unroll
-            for (int c = 0; c < NH; c += STEP) {
-                float y[STEP];
-                tmem_load(my_s + c, y);
-#pragma unroll
-                for (int i = 0; i < STEP; ++i) x[c + i] = y[i];
-            }
-            float hi = kNoMax;
-            const bool masked = cnt < 128 || !packed;
-            if (masked) {
-#pragma unroll
-                for (int i = 0; i < NH; ++i) {
-                    const int c = half * NH + i;
-                    bool see = valid;
-                    if (draft >= 0) {
-                        const int r = row0 + c, node = r >> a.gshift;
-                        see = r < row_end;
-                        if (see) see = a.mask ? a.mask[((int64_t)b * a.nodes + node) * a.nodes + draft] != 0 : draft <= node;
-                    }
-                    const float2 g = col[c];
-                    x[i] = see ? fmaf(x[i], f * g.x, lv) : -INFINITY;
-                    hi = fmaxf(hi, x[i] + g.y);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < NH; ++i) {
-                    const float2 g = col[half * NH + i];
-                    x[i] = fmaf(x[i], f * g.x, lv);
-                    hi = fmaxf(hi, x[i] + g.y);
-                }
-            }
-            if (__syncthreads_or(hi > kReach)) {
-                // the columns' maxima over the tile, and the new references
-#pragma unroll
-                for (int i = 0; i < NH; ++i) {
-                    const float m = warp_max(x[i]);
-                    if (lane == 0) cmax[quad][half * NH + i] = m;
-                }
-                __syncthreads();
-                if (tid < N) {
-                    const float m = fmaxf(fmaxf(cmax[0][tid], cmax[1][tid]), fmaxf(cmax[2][tid], cmax[3][tid])) - kHead;
-                    const float old = -col[tid].y, now = fmaxf(old, m);
-                    col[tid].y = -now;
-                    fac[tid] = tree_exp2(old - now);
-                }
-                __syncthreads();
-#pragma unroll
-                for (int i = 0; i < NH; ++i) l[i] *= fac[half * NH + i];
-                if (have_o) {
-#pragma unroll
-                    for (int d = 0; d < S::kDN; ++d)
-#pragma unroll
-                        for (int c = 0; c < NH; c += STEP) {
-                            float o[STEP];
-                            const uint32_t at = tm_o + d * N + (static_cast<uint32_t>(32 * quad) << 16) + half * NH + c;
-                            tmem_load(at, o);
-#pragma unroll
-                            for (int i = 0; i < STEP; ++i) o[i] *= fac[half * NH + c + i];
-                            tmem_store(at, o);
+                publish(&sh.v_full);
+                if (empty && lane == 0) mbar_arrive(empty);
+            };
+            do {
+                for (int tile = w.first; w.live && tile < w.end; ++tile, ++it) {
+                    wait(&sh.s_empty[it & 1], (it >> 1) + 1);       // the factors of two tiles before are read
+                    if (tile >= w.s.packed) {
+                        const int r0 = (tile - w.s.packed) * 128, cnt = w.raw_count(tile), held = w.s.n - w.s.qn - r0;
+                        wait(&sh.k_empty, it + 1);
+                        raw_rows<D, DT>(a, w.b, w.h, w.s, r0, cnt, W, rows_scheme, kt, nullptr, sh.kf[it & 1], sh.vl[it & 1], &sh.odd, 0, ut);
+                        raw_rows<D, DT>(a, w.b, w.h, w.s, r0, cnt, W, rows_scheme, nullptr, nullptr, sh.kf[it & 1], sh.vl[it & 1], &sh.odd, 1, ut);
+                        if (rope) {
+                            bar_sync(1, DT);
+                            turn_keys<D, DT>(kt, sh.wt, (int64_t)w.s.qn + r0, held < cnt ? held : cnt, false, ut);
                         }
+                        publish(&sh.k_full);
+                        wait(&sh.pv_done, it + 1);
+                        raw_rows<D, DT>(a, w.b, w.h, w.s, r0, cnt, W, rows_scheme, nullptr, vt, sh.kf[it & 1], sh.vl[it & 1], &sh.odd, 1, ut);
+                        publish(&sh.v_full);
+                        continue;
+                    }
+                    const int cnt = w.packed_count(a, tile);
+                    const int64_t t0 = (int64_t)tile * a.TT;
+                    if (a.stages == 0) {
+                        // records too large to pass through shared memory next to the tiles
+                        if (ut < 8 && ut * lo.G < cnt) {
+                            int64_t off = group_offset(lo, a.layer, w.b, w.h, (int64_t)tile * a.TG + ut);
+                            if (off < 0) {
+                                atomicOr(reinterpret_cast<uint32_t*>(a.ws), KVQ_STATUS_BAD_PAGE);
+                                off = lo.data_off + (((int64_t)a.layer * H + w.h) * lo.PG + (tile * a.TG + ut) % lo.PG) * lo.rec;
+                            }
+                            sh.recs[it & 1][ut] = a.cache + off;
+                        }
+                        bar_sync(1, DT);
+                        PackedTile<false> t;
+                        t.recs = sh.recs[it & 1];
+                        t.cnt = cnt;
+                        t.t0 = t0;
+                        kivi_tile(t, nullptr);
+                        continue;
+                    }
+                    const uint32_t sl = a.stages == 2 ? staged & 1 : 0, ph = a.stages == 2 ? staged >> 1 : staged;
+                    ++staged;
+                    const uint8_t* raw = stage + sl * a.stage_bytes;
+                    wait(&sh.stage_full[sl], ph);
+                    if (kivi) {
+                        PackedTile<true> t;
+                        t.base = raw;
+                        t.stride = lo.rec;
+                        t.cnt = cnt;
+                        t.t0 = t0;
+                        kivi_tile(t, &sh.stage_empty[sl]);
+                        continue;
+                    }
+                    if (ut < 128) {
+                        const int tok = fp8 ? packed_token(ut) : ut;
+                        float f = 0.0f, lv = 0.0f;
+                        if (fp8) {
+                            const float* sc = fp8_scale(a, w.h);
+                            f = sc[0];
+                            lv = fast_log2(fabsf(sc[1]));
+                        } else if (tok < cnt) {
+                            const float* sc = reinterpret_cast<const float*>(raw + 256 * row_bytes);
+                            f = sc[tok];
+                            lv = fast_log2(sc[128 + tok]);
+                        }
+                        sh.kf[it & 1][ut] = f;
+                        sh.vl[it & 1][ut] = fmaxf(lv, -110.0f);     // (a scale of 0 belongs to codes of 0)
+                    }
+                    wait(&sh.k_empty, it + 1);
+                    const bool e4m3 = lo.scheme == KVQ_SCHEME_FP8_E4M3, int8 = lo.scheme == KVQ_SCHEME_INT8;
+                    if (fp8) fp8_keys<D, DT>(raw, cnt, e4m3, kt, ut);
+                    else rows_codes<D, DT>(raw, cnt, 0, int8, kt, ut);
+                    publish(&sh.k_full);
+                    wait(&sh.pv_done, it + 1);
+                    const uint8_t* vraw = raw + 128 * row_bytes;
+                    if (fp8) fp8_values<D, DT>(vraw, cnt, e4m3, fp8_scale(a, w.h)[1] < 0.0f, vt, ut);
+                    else rows_codes<D, DT>(vraw, cnt, 1, int8, vt, ut);
+                    publish(&sh.v_full);
+                    if (lane == 0) mbar_arrive(&sh.stage_empty[sl]);
                 }
+            } while (w.next(a, N));
+        } else if (warp == S::kSoft + S::kUnpack) {
+            // ======================================================================= product
+            if (lane == 0) {
+                uint32_t it = 0, seg = 0;
+                const uint64_t dk = mma_desc(smem_addr(kt), D / 8 * kCoreBytes), dq = mma_desc(smem_addr(qt), D / 8 * kCoreBytes);
+                const uint64_t dp = mma_desc(smem_addr(pt), 16 * kCoreBytes);
+                // the scores of tile i
+                auto score = [&](uint32_t i) {
+                    wait(&sh.k_full, i);
+                    wait(&sh.s_empty[i & 1], (i >> 1) + 1);
+                    tmem_fence_after();
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k)
+                        mma_f16(tm_s + (i & 1) * N, dk + k * (2 * kCoreBytes >> 4), dq + k * (2 * kCoreBytes >> 4),
+                                mma_idesc(128, N, false, false), k > 0);
+                    mma_commit(&sh.k_empty);
+                    mma_commit(&sh.s_full[i & 1]);
+                    mbar_arrive(&sh.s_full[i & 1]);     // hands the tokens' factors on, too
+                };
+                do {
+                    if (!w.live) continue;
+                    wait(&sh.q_full, seg++);
+                    score(it);
+                    for (int tile = w.first; tile < w.end; ++tile, ++it) {
+                        if (tile + 1 < w.end) score(it + 1);
+                        const bool packed = tile < w.s.packed, mn = !packed || rows_scheme;
+                        const int steps = ((packed ? w.packed_count(a, tile) : w.raw_count(tile)) + 15) >> 4;
+                        wait(&sh.v_full, it);
+                        wait(&sh.p_full, it);
+                        tmem_fence_after();
+#pragma unroll
+                        for (int d = 0; d < S::kDN; ++d) {
+                            const uint64_t dv = mma_desc(smem_addr(vt) + d * 32768, 16 * kCoreBytes);
+                            for (int k = 0; k < steps; ++k)
+                                mma_f16(tm_o + d * N, dv + k * (2 * kCoreBytes >> 4), dp + k * (2 * kCoreBytes >> 4),
+                                        mma_idesc(128, N, mn, true), tile > w.first || k > 0);
+                        }
+                        mma_commit(&sh.pv_done);
+                    }
+                } while (w.next(a, N));
+                mma_commit(&sh.done);
+                if (!mbar_wait_clock(&sh.done, 0)) atomicOr(reinterpret_cast<uint32_t*>(a.ws), KVQ_STATUS_TIMEOUT);
             }
-#pragma unroll
-            for (int c = 0; c < NH; c += 8) {
-                uint32_t p[4];
-#pragma unroll
-                for (int i = 0; i < 8; i += 2) {
-                    const float p0 = tree_exp2(x[c + i] + col[half * NH + c + i].y);
-                    const float p1 = tree_exp2(x[c + i + 1] + col[half * NH + c + i + 1].y);
-                    l[c + i] = fmaf(p0, inv, l[c + i]);
-                    l[c + i + 1] = fmaf(p1, inv, l[c + i + 1]);
-                    p[i / 2] = h2_as_u32(__floats2half2_rn(p0, p1));
-                }
-                *reinterpret_cast<uint4*>(pt + ((half * NH + c) >> 3) * (16 * kCoreBytes) + (row >> 3) * kCoreBytes + (row & 7) * 16) =
-                    make_uint4(p[0], p[1], p[2], p[3]);
-            }
-            smem_to_async();
-            tmem_fence_before();
-            __syncthreads();
-            if (tid == 0) {
-                tmem_fence_after();
-                const bool mn = !packed || rows_scheme;                 // values with channels inside a row
-                const uint64_t db = mma_desc(smem_addr(pt), 16 * kCoreBytes);
-#pragma unroll
-                for (int d = 0; d < S::kDN; ++d) {
-                    const uint64_t da = mma_desc(smem_addr(vt) + d * 32768, 16 * kCoreBytes);
-                    for (int k = 0; k < steps; ++k)
-                        mma_f16(tm_o + d * N, da + k * (2 * kCoreBytes >> 4), db + k * (2 * kCoreBytes >> 4),
-                                mma_idesc(128, N, mn, true), have_o || k > 0);
-                }
-                mma_commit(&bar_pv);
-            }
-            pv_open = true;
-            have_o = true;
-        }
-        // ------------------------------------------------------------ the segment's result
-        const bool whole = first == 0 && end == unit_tiles;
-        const int64_t unit = ((int64_t)b * H + h) * a.RT + rt;
-        const int64_t slot = blockIdx.x + unit;
-        if (pv_open) {
-            wait(&bar_pv, ph_pv);
-            ph_pv ^= 1;
-            pv_open = false;
-        }
-        tmem_fence_after();
-        const bool odd = __syncthreads_or(nonfinite);
-        // the sums over a column's tokens
-#pragma unroll
-        for (int i = 0; i < NH; ++i) {
-            float v = l[i];
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-            if (lane == 0) lsum[quad][half * NH + i] = v;
-        }
-        __syncthreads();
-        if (tid < N) {
-            // rows of padding nodes saw the cached tokens with a query of 0: their output is 0
-            const float v = live && row0 + tid < row_end ? (lsum[0][tid] + lsum[1][tid]) + (lsum[2][tid] + lsum[3][tid]) : 0.0f;
-            if (whole) {
-                fac[tid] = v != 0.0f ? 1.0f / v : 0.0f;
-            } else {
-                fac[tid] = v != 0.0f ? 1.0f : 0.0f;
-                reinterpret_cast<float2*>(a.ws + a.ml_off)[slot * N + tid] = make_float2(-col[tid].y, v);
-            }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int d = 0; d < S::kDN; ++d) {
-            const int ch0 = 128 * d + 32 * quad;
-            if (ch0 >= D) continue;
-            // lane -> channel: the order of the tile's value rows
-            const int c0 = rows_scheme ? place_channel(ch0 + lane, W, D) : ch0 + lane;
-#pragma unroll
-            for (int c = 0; c < NH; c += STEP) {
-                float o[STEP];
-                if (live)
-                    tmem_load(tm_o + d * N + (static_cast<uint32_t>(32 * quad) << 16) + half * NH + c, o);
-#pragma unroll
-                for (int i = 0; i < STEP; ++i) {
-                    const int cc = half * NH + c + i, r = row0 + cc;
-                    if (r >= a.rows) continue;
-                    const float fc = fac[cc];
-                    float v = fc != 0.0f ? o[i] * fc : 0.0f;
-                    if (odd && r < row_end) {   // drafts whose value is not finite, in the rows that see them
-                        const int node = r >> a.gshift;
-                        for (int j = 0; j < s.nodes; ++j) {
-                            const float y = __bfloat162float(a.v[(((int64_t)b * a.nodes + j) * H + h) * D + c0]);
-                            if (fabsf(y) < INFINITY) continue;
-                            if (a.mask ? a.mask[((int64_t)b * a.nodes + node) * a.nodes + j] != 0 : j <= node) v += y;
+        } else if (lane == 0 && a.stages > 0) {
+            // ========================================================================== copy
+            uint32_t staged = 0;
+            do {
+                for (int tile = w.first; w.live && tile < w.end && tile < w.s.packed; ++tile) {
+                    const uint32_t sl = a.stages == 2 ? staged & 1 : 0, ph = a.stages == 2 ? staged >> 1 : staged;
+                    wait(&sh.stage_empty[sl], ph + 1);
+                    if (dead()) break;
+                    ++staged;
+                    uint8_t* to = stage + sl * a.stage_bytes;
+                    uint64_t* bar = &sh.stage_full[sl];
+                    const int cnt = w.packed_count(a, tile);
+                    const int64_t t0 = (int64_t)tile * a.TT;
+                    if (kivi) {
+                        const int g0 = tile * a.TG, all = w.s.qn / lo.G - g0, ng = all < a.TG ? all : a.TG;
+                        mbar_arrive_expect_tx(bar, static_cast<uint32_t>(ng * lo.rec));
+                        if (lo.PG == 0) {
+                            bulk_copy_g2s(to, a.cache + group_offset(lo, a.layer, w.b, w.h, g0), ng * lo.rec, bar);
+                        } else {
+                            for (int g = 0; g < ng; ++g) {
+                                int64_t off = group_offset(lo, a.layer, w.b, w.h, g0 + g);
+                                if (off < 0) {  // a table entry outside the pool: page 0 in its place, reported
+                                    atomicOr(reinterpret_cast<uint32_t*>(a.ws), KVQ_STATUS_BAD_PAGE);
+                                    off = lo.data_off + (((int64_t)a.layer * H + w.h) * lo.PG + (g0 + g) % lo.PG) * lo.rec;
+                                }
+                                bulk_copy_g2s(to + g * lo.rec, a.cache + off, lo.rec, bar);
+                            }
+                        }
+                    } else {
+                        const int c16 = (cnt + 15) & ~15;
+                        const uint8_t* base = a.cache + lo.data_off + unit_index(lo, a.layer, w.b, w.h) * lo.unit;
+                        const uint32_t bytes = static_cast<uint32_t>(c16 * row_bytes);
+                        mbar_arrive_expect_tx(bar, 2 * bytes + (rows_scheme ? 8 * c16 : 0));
+                        bulk_copy_g2s(to, base + t0 * row_bytes, bytes, bar);
+                        bulk_copy_g2s(to + 128 * row_bytes, base + (lo.T16 + t0) * row_bytes, bytes, bar);
+                        if (rows_scheme) {
+                            const uint8_t* sc = base + 2 * (int64_t)lo.T16 * row_bytes;
+                            bulk_copy_g2s(to + 256 * row_bytes, sc + 4 * t0, 4 * c16, bar);
+                            bulk_copy_g2s(to + 256 * row_bytes + 512, sc + 4 * (lo.T16 + t0), 4 * c16, bar);
                         }
                     }
-                    if (whole)
-                        a.out[(((int64_t)b * a.nodes + (r >> a.gshift)) * lo.Hq + h * gqa + (r & (gqa - 1))) * D + c0] =
-                            __float2bfloat16_rn(v);
-                    else
-                        reinterpret_cast<float*>(a.ws + a.o_off)[(slot * N + cc) * D + c0] = v;
                 }
-            }
-        }
-        tmem_fence_before();
-        __syncthreads();
-        tmem_fence_after();
-        // ------------------------------------------------------------ the next unit
-        left -= end - first;
-        if (tile >= unit_tiles) {
-            tile = 0;
-            if (++rt == a.RT) {
-                rt = 0;
-                if (++h == H) {
-                    h = 0;
-                    ++b;
-                    if (left > 0) s = tree_seq(a, b, N);
-                }
-            }
+            } while (w.next(a, N));
+            // where a wait gave up, the copies in flight land before the block ends
+            if (dead())
+                for (uint32_t i = staged > static_cast<uint32_t>(a.stages) ? staged - a.stages : 0; i < staged; ++i)
+                    mbar_wait_clock(&sh.stage_full[a.stages == 2 ? i & 1 : 0], (a.stages == 2 ? i >> 1 : i) & 1);
         }
     }
     __syncthreads();
@@ -1171,7 +1345,7 @@ __global__ void __launch_bounds__(kTreeThreads, TreeSmem<N, D>::kBlocks) k_tree(
 // columns of one row tile: it finds the blocks whose shares meet the row tile's tiles, and for
 // each column sums their O 2^(m - M) and l 2^(m - M).
 template <int N, int D>
-__global__ void __launch_bounds__(kTreeThreads) k_tree_merge(const __grid_constant__ TreeArgs a) {
+__global__ void __launch_bounds__(kMergeThreads) k_tree_merge(const __grid_constant__ TreeArgs a) {
     constexpr int CW = N < 32 ? N / 2 : 16;
     __shared__ int64_t scan[8], start;
     const Layout& lo = a.lo;
@@ -1182,12 +1356,12 @@ __global__ void __launch_bounds__(kTreeThreads) k_tree_merge(const __grid_consta
     const int b = static_cast<int>(bh / lo.H), h = static_cast<int>(bh % lo.H);
     const int row0 = rt * N;
     // the token counts are not written by the attention: the plan needs no wait for it
-    const int64_t total = tree_total(a, N, scan);
+    const int64_t total = tree_total<kMergeThreads>(a, N, scan);
     int64_t base = 0;
-    for (int b0 = 0; b0 <= b; b0 += kTreeThreads) {
+    for (int b0 = 0; b0 <= b; b0 += kMergeThreads) {
         const int bb = b0 + threadIdx.x;
         int64_t sum;
-        const int64_t at = base + block_scan(bb < lo.B ? lo.H * tree_head_tiles(a, tree_seq(a, bb, N)) : 0, scan, &sum);
+        const int64_t at = base + block_scan<kMergeThreads>(bb < lo.B ? lo.H * tree_head_tiles(a, tree_seq(a, bb, N)) : 0, scan, &sum);
         if (bb == b) start = at;
         base += sum;
     }
@@ -1205,7 +1379,7 @@ __global__ void __launch_bounds__(kTreeThreads) k_tree_merge(const __grid_consta
     if (rt >= s.live || j0 == j1) return;
     const float2* ml = reinterpret_cast<const float2*>(a.ws + a.ml_off);
     const float* po = reinterpret_cast<const float*>(a.ws + a.o_off);
-    for (int i = threadIdx.x; i < CW * D; i += kTreeThreads) {
+    for (int i = threadIdx.x; i < CW * D; i += kMergeThreads) {
         const int c = c0 + i / D, ch = i % D, r = row0 + c;
         if (r >= a.rows) continue;
         float M = -INFINITY;
@@ -1230,10 +1404,9 @@ __global__ void __launch_bounds__(kTreeThreads) k_tree_merge(const __grid_consta
     }
 }
 
-// `stage`: bytes of shared memory that a tile's packed bytes pass through.
-int launch_tree_d32(TreeArgs& a, int N, int64_t stage, cudaStream_t stream);
-int launch_tree_d64(TreeArgs& a, int N, int64_t stage, cudaStream_t stream);
-int launch_tree_d128(TreeArgs& a, int N, int64_t stage, cudaStream_t stream);
-int launch_tree_d256(TreeArgs& a, int N, int64_t stage, cudaStream_t stream);
+int launch_tree_d32(TreeArgs& a, int N, cudaStream_t stream);
+int launch_tree_d64(TreeArgs& a, int N, cudaStream_t stream);
+int launch_tree_d128(TreeArgs& a, int N, cudaStream_t stream);
+int launch_tree_d256(TreeArgs& a, int N, cudaStream_t stream);
 
 }  // namespace kvq

@@ -7,17 +7,18 @@
 namespace kvq {
 
 template <int N, int D>
-int launch_tree_t(TreeArgs& a, int64_t stage, cudaStream_t stream) {
-    const int64_t smem = TreeSmem<N, D>::kStage + stage;
+int launch_tree_t(TreeArgs& a, cudaStream_t stream) {
+    constexpr int NT = TreeShape<N, D>::kThreads;
+    const int64_t smem = TreeShape<N, D>::kStage + (int64_t)a.stages * a.stage_bytes;
     int nb = 0;
-    const int rc = decode_blocks(reinterpret_cast<const void*>(k_tree<N, D>), kTreeThreads, smem, &nb);
+    const int rc = decode_blocks(reinterpret_cast<const void*>(k_tree<N, D>), NT, smem, &nb);
     if (rc != KVQ_OK) return rc;
     a.NB = nb < kMaxTreeBlocks ? nb : kMaxTreeBlocks;
-    if (launch_dependent(k_tree<N, D>, dim3(a.NB), dim3(kTreeThreads), static_cast<size_t>(smem), stream, a) != cudaSuccess)
+    if (launch_dependent(k_tree<N, D>, dim3(a.NB), dim3(NT), static_cast<size_t>(smem), stream, a) != cudaSuccess)
         return KVQ_ERR_CUDA;
     const int64_t units = (int64_t)a.lo.B * a.lo.H * a.RT;
     constexpr int CW = N < 32 ? N / 2 : 16;
-    return launch_dependent(k_tree_merge<N, D>, dim3(static_cast<unsigned>(units * (N / CW))), dim3(kTreeThreads), 0, stream,
+    return launch_dependent(k_tree_merge<N, D>, dim3(static_cast<unsigned>(units * (N / CW))), dim3(kMergeThreads), 0, stream,
                             a) == cudaSuccess
                ? KVQ_OK
                : KVQ_ERR_CUDA;
