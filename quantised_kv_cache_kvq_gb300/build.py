@@ -54,10 +54,25 @@ UNITS = {
     "kvq_rotary.cu": [],
     "kvq_read.cu": [],
     "kvq_tree.cu": [],
-    "kvq_tree_d32.cu": [],
-    "kvq_tree_d64.cu": [],
-    "kvq_tree_d128.cu": [],
-    "kvq_tree_d256.cu": [],
+    "kvq_tree_rows_d32.cu": [],
+    "kvq_tree_fp8_d32.cu": [],
+    "kvq_tree_kivi2_d64.cu": [],
+    "kvq_tree_kivi4_d64.cu": [],
+    "kvq_tree_kivi8_d64.cu": [],
+    "kvq_tree_rows_d64.cu": [],
+    "kvq_tree_fp8_d64.cu": [],
+    "kvq_tree_kivi2_d128.cu": [],
+    "kvq_tree_kivi4_d128.cu": [],
+    "kvq_tree_kivi8_d128.cu": [],
+    "kvq_tree_inplace_d128.cu": [],
+    "kvq_tree_rows_d128.cu": [],
+    "kvq_tree_fp8_d128.cu": [],
+    "kvq_tree_kivi2_d256.cu": [],
+    "kvq_tree_kivi4_d256.cu": [],
+    "kvq_tree_kivi8_d256.cu": [],
+    "kvq_tree_inplace_d256.cu": [],
+    "kvq_tree_rows_d256.cu": [],
+    "kvq_tree_fp8_d256.cu": [],
 }
 
 

@@ -7,6 +7,27 @@
 #include "kvq_tree.cuh"
 
 namespace kvq {
+
+int launch_tree_rows_d32(TreeArgs& a, int N, cudaStream_t stream);
+int launch_tree_fp8_d32(TreeArgs& a, int N, cudaStream_t stream);
+int launch_tree_kivi2_d64(TreeArgs& a, int N, cudaStream_t stream);
+int launch_tree_kivi4_d64(TreeArgs& a, int N, cudaStream_t stream);
+int launch_tree_kivi8_d64(TreeArgs& a, int N, cudaStream_t stream);
+int launch_tree_rows_d64(TreeArgs& a, int N, cudaStream_t stream);
+int launch_tree_fp8_d64(TreeArgs& a, int N, cudaStream_t stream);
+int launch_tree_kivi2_d128(TreeArgs& a, int N, cudaStream_t stream);
+int launch_tree_kivi4_d128(TreeArgs& a, int N, cudaStream_t stream);
+int launch_tree_kivi8_d128(TreeArgs& a, int N, cudaStream_t stream);
+int launch_tree_inplace_d128(TreeArgs& a, int N, cudaStream_t stream);
+int launch_tree_rows_d128(TreeArgs& a, int N, cudaStream_t stream);
+int launch_tree_fp8_d128(TreeArgs& a, int N, cudaStream_t stream);
+int launch_tree_kivi2_d256(TreeArgs& a, int N, cudaStream_t stream);
+int launch_tree_kivi4_d256(TreeArgs& a, int N, cudaStream_t stream);
+int launch_tree_kivi8_d256(TreeArgs& a, int N, cudaStream_t stream);
+int launch_tree_inplace_d256(TreeArgs& a, int N, cudaStream_t stream);
+int launch_tree_rows_d256(TreeArgs& a, int N, cudaStream_t stream);
+int launch_tree_fp8_d256(TreeArgs& a, int N, cudaStream_t stream);
+
 namespace {
 
 struct TreePlan {
@@ -16,15 +37,17 @@ struct TreePlan {
 };
 
 // Bytes of the operand tiles of k_tree<N, D> (TreeShape), and what a block may have next to the
-// kernel's static arrays (under 8 KiB).
+// kernel's static arrays (under 8 KiB); with two blocks per SM, half of 228 KiB less 1 KiB
+// reserved each and those arrays (under 4 KiB).
 int64_t tile_bytes(int N, int D) { return 256 * D + (D > 128 ? 65536 : 32768) + 2 * N * D + 256 * N; }
-constexpr int64_t kTreeSmemLimit = 219 * 1024;
+constexpr int64_t kTreeSmemLimit = 219 * 1024, kTreeSmemHalf = 109 * 1024;
 
 // The row tile: the fewest columns, 16 to 128, that hold all queries of a KV head, or 128 (64
 // for heads of 256 channels, whose tiles are twice as large).  The packed bytes of the next two
 // tiles (else the next one) pass through shared memory where they fit next to the operand
-// tiles, with half the columns if that makes the room; else (KIVI records with many outliers,
-// or of 256 channels at 8 bits) the kernel reads them in place.
+// tiles -- two only if that costs no resident block -- with half the columns if that makes the
+// room; else (KIVI records with many outliers, or of 256 channels at 8 bits) the kernel reads
+// them in place.
 int tree_plan(const kvq_config* cfg, int nodes, TreePlan* p) {
     const int rc = make_layout(cfg, cfg->max_tokens, &p->lo);
     if (rc != KVQ_OK) return rc;
@@ -47,7 +70,8 @@ int tree_plan(const kvq_config* cfg, int nodes, TreePlan* p) {
         tile_bytes(p->N / 2, D) + p->stage <= kTreeSmemLimit)
         p->N /= 2;
     const int64_t room = kTreeSmemLimit - tile_bytes(p->N, D);
-    p->stages = room >= 2 * p->stage ? 2 : room >= p->stage ? 1 : 0;
+    const int64_t half = p->N > 64 || D > 128 ? -1 : kTreeSmemHalf - tile_bytes(p->N, D);
+    p->stages = half >= p->stage ? (half >= 2 * p->stage ? 2 : 1) : room >= 2 * p->stage ? 2 : room >= p->stage ? 1 : 0;
     if (p->stages == 0) {
         if (lo.scheme != KVQ_SCHEME_KIVI) return KVQ_ERR_UNSUPPORTED;
         p->stage = 0;
@@ -58,6 +82,30 @@ int tree_plan(const kvq_config* cfg, int nodes, TreePlan* p) {
     p->o_off = align256(p->ml_off + slots * p->N * 8);
     p->bytes = align256(p->o_off + slots * p->N * D * 4);
     return KVQ_OK;
+}
+
+int launch_tree(TreeArgs& a, int N, cudaStream_t st) {
+    const int D = a.lo.D;
+    if (is_rows(a.lo.scheme))
+        return D == 32 ? launch_tree_rows_d32(a, N, st) : D == 64 ? launch_tree_rows_d64(a, N, st)
+             : D == 128 ? launch_tree_rows_d128(a, N, st) : launch_tree_rows_d256(a, N, st);
+    if (is_fp8(a.lo.scheme))
+        return D == 32 ? launch_tree_fp8_d32(a, N, st) : D == 64 ? launch_tree_fp8_d64(a, N, st)
+             : D == 128 ? launch_tree_fp8_d128(a, N, st) : launch_tree_fp8_d256(a, N, st);
+    if (a.stages == 0)
+        return D == 128 ? launch_tree_inplace_d128(a, N, st) : D == 256 ? launch_tree_inplace_d256(a, N, st)
+                                                                        : KVQ_ERR_UNSUPPORTED;
+    switch (a.lo.bits) {
+        case 2:
+            return D == 64 ? launch_tree_kivi2_d64(a, N, st) : D == 128 ? launch_tree_kivi2_d128(a, N, st)
+                                                                        : launch_tree_kivi2_d256(a, N, st);
+        case 4:
+            return D == 64 ? launch_tree_kivi4_d64(a, N, st) : D == 128 ? launch_tree_kivi4_d128(a, N, st)
+                                                                        : launch_tree_kivi4_d256(a, N, st);
+        default:
+            return D == 64 ? launch_tree_kivi8_d64(a, N, st) : D == 128 ? launch_tree_kivi8_d128(a, N, st)
+                                                                        : launch_tree_kivi8_d256(a, N, st);
+    }
 }
 
 }  // namespace
@@ -109,6 +157,8 @@ int kvq_tree_attention(const kvq_config* cfg, const void* cache, int32_t layer, 
     a.TG = a.lo.scheme == KVQ_SCHEME_KIVI ? p.TT / a.lo.G : 0;
     a.gvshift = 0;
     while ((1 << a.gvshift) < a.lo.Gv) ++a.gvshift;
+    a.pieces = a.lo.scheme == KVQ_SCHEME_KIVI ? (a.lo.D + a.lo.NGv * a.lo.G) / 8 : 1;
+    a.pieces_inverse = static_cast<uint32_t>((0x100000000ull + a.pieces - 1) / a.pieces);
     for (int i = 0; i < 8; ++i) a.group_of[i] = a.TG > 0 && 16 * i < p.TT ? 16 * i / a.lo.G : 0;
     a.stages = p.stages;
     a.stage_bytes = static_cast<int>(p.stage);
@@ -118,13 +168,7 @@ int kvq_tree_attention(const kvq_config* cfg, const void* cache, int32_t layer, 
         for (int i = 0; i < a.lo.D / 2; ++i)
             a.rope_w[i] = static_cast<float>(std::pow(static_cast<double>(a.lo.rope_base), -2.0 * i / a.lo.D));
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    switch (a.lo.D) {
-        case 32: return kvq::launch_tree_d32(a, p.N, st);
-        case 64: return kvq::launch_tree_d64(a, p.N, st);
-        case 128: return kvq::launch_tree_d128(a, p.N, st);
-        case 256: return kvq::launch_tree_d256(a, p.N, st);
-        default: return KVQ_ERR_UNSUPPORTED;
-    }
+    return kvq::launch_tree(a, p.N, st);
 }
 
 }  // extern "C"

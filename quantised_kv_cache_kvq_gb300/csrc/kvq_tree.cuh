@@ -8,14 +8,14 @@
 // with the tokens (and the channels) on the instruction's M side, so that its cost follows the
 // number of queries, 16 to 128, and a cache byte is dequantised once for all of them.
 //
-// One block per SM, its warps in four roles that hand tiles to each other through mbarriers:
-//   copy      one thread: bulk copies of the packed bytes of the next tiles
-//   unpack    packed bytes -> K and V operand tiles in binary16
-//   product   one thread: issues both products
-//   softmax   scores (TMEM) -> weights P (shared memory), references, sums, results;
-//             a thread owns a token (a TMEM lane of S^T) and some of the columns
-// While the softmax of a tile runs, the next tile's keys are unpacked and its scores computed;
-// its values follow once the weights' product has read the tile's.
+// Per tile a block unpacks the keys, issues the scores' product, unpacks the values while it
+// runs, takes the scores out of TMEM, writes the weights to shared memory and issues their
+// product, which runs under the next tile's keys.  Two blocks share an SM where their tiles fit
+// (heads of up to 128 channels, up to 64 columns), so that one computes while the other waits.
+// (Warps in roles that hand tiles on through mbarriers -- copy, check, keys, values, product,
+// softmax -- measured slower: 133 us against the figure below for 16 drafts over a 2-bit layer
+// of 8 x 4096 tokens.  The roles' code, side by side, missed the instruction cache, their
+// waits took issue slots, and 20 to 24 warps left too few registers.)
 //
 // Softmax, in base 2.  A token's value row is stored in binary16 as v 2^-e (or as its code),
 // v = stored * s; the weight that multiplies it is P = 2^(x + log2 s - m) with a running
@@ -49,6 +49,8 @@ struct TreeArgs {
     int NB;                             // blocks of the launch
     int TT, TG;                         // tokens, and groups, of a full packed tile
     int gvshift;                        // log2 of the value group (it divides a power of two)
+    int pieces;                         // KIVI: pieces of 8 key and value parameters of a group
+    uint32_t pieces_inverse;            // 2^32 / pieces, rounded up
     int group_of[8];                    // KIVI: the group of a tile's 16-token piece
     int stages, stage_bytes;            // buffers that a tile's packed bytes pass through (0: none)
     const __nv_bfloat16 *q, *k, *v;
@@ -231,7 +233,6 @@ struct PackedTile {
     int stride;
     const uint8_t* const* recs;   // not STAGED: the records' places
     int cnt;                      // tokens
-    int64_t t0;                   // the first one
     __device__ __forceinline__ const uint8_t* rec(int g) const {
         if constexpr (STAGED) return base + g * stride;
         else return recs[g];
@@ -246,7 +247,7 @@ __device__ __forceinline__ void kivi_keys(const TreeArgs& a, const Tile t, uint8
     constexpr int QUADS = D / 64, PER = 16 * QUADS / (DT / 32);       // octets of a warp
     const Layout& lo = a.lo;
     const int warp = tid >> 5, lane = tid & 31;
-    const int unit = (warp % QUADS) * 4 + (lane >> 3), o0 = (warp / QUADS) * PER;
+    const int unit = (warp % QUADS) * 4 + (((lane >> 3) + lane) & 3), o0 = (warp / QUADS) * PER;
     uint32_t s[8], z[8];
     int have = -1;
 #pragma unroll 2
@@ -333,23 +334,48 @@ __device__ __forceinline__ void kivi_values(const TreeArgs& args, const Tile t, 
     }
 }
 
-// Largest |value| that the keys (kv = 0) or values of the tile's groups can have, over this
-// thread's share of their parameters; what is not finite is left out.
+// Whether some |value| that the tile's keys or values can have reaches 2^15, over a thread's
+// share of their parameters (in binary16: levels * s + |z|, an infinity counts).  Piece i of 8
+// parameters of a tile lies `piece` bytes into its group's record.
 template <int DT, typename Tile>
-__device__ __forceinline__ float kivi_bound(const Layout& lo, const Tile t, int kv, int tid) {
+__device__ __forceinline__ bool kivi_wide(const TreeArgs& a, const Tile& t, int tid) {
+    const Layout& lo = a.lo;
+    const __half2 levels = __float2half2_rn(static_cast<float>((1 << lo.bits) - 1));
+    __half2 top = __float2half2_rn(0.0f);
+    uint32_t side_top = 0;
+    for (int i = tid; i < a.TG * a.pieces; i += DT) {
+        const int g = static_cast<int>(__umulhi(i, a.pieces_inverse));      // i / pieces
+        if (g * lo.G >= t.cnt) break;
+        const int at = i - g * a.pieces, kpieces = lo.D / 8;
+        const bool v = at >= kpieces;
+        const uint8_t* p = t.rec(g) + lo.kc + lo.vc + 16 * at + (v ? 2 * lo.D : 0);
+        const uint4 s = *reinterpret_cast<const uint4*>(p), z = *reinterpret_cast<const uint4*>(p + (v ? 16 * (a.pieces - kpieces) : 2 * lo.D));
+        const uint32_t sw[4] = {s.x, s.y, s.z, s.w}, zw[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) top = __hmax2(top, __hfma2(levels, u32_as_h2(sw[j]), __habs2(u32_as_h2(zw[j]))));
+    }
+    if (lo.K > 0)
+        for (int g = 0; g * lo.G < t.cnt; ++g) {
+            const uint32_t* side = reinterpret_cast<const uint32_t*>(t.rec(g) + lo.kc + lo.vc + lo.kp + lo.vp);
+            for (int i = tid; i < (lo.ko + lo.vo) / 4; i += DT) side_top = max(side_top, side[i] & 0x7fff0000u);
+        }
+    const uint32_t h = h2_as_u32(top);
+    return (h & 0xffffu) >= 0x7800u || (h >> 16) >= 0x7800u || side_top >= 0x47000000u;
+}
+// Their largest finite |value|, of the keys (kv = 0) or values, over a thread's share.
+template <int DT, typename Tile>
+__device__ __noinline__ float kivi_bound(const Layout& lo, const Tile t, int kv, int lane) {
     const float levels = static_cast<float>((1 << lo.bits) - 1);
     const int pairs = kv ? lo.NGv * lo.G : lo.D;
     float top = 0.0f;
     for (int g = 0; g * lo.G < t.cnt; ++g) {
         const __half* par = reinterpret_cast<const __half*>(t.rec(g) + lo.kc + lo.vc + (kv ? lo.kp : 0));
         const uint32_t* side = reinterpret_cast<const uint32_t*>(t.rec(g) + lo.kc + lo.vc + lo.kp + lo.vp + (kv ? lo.ko : 0));
-        for (int i = 2 * tid; i < pairs; i += 2 * DT) {
-            const float2 s = __half22float2(*reinterpret_cast<const __half2*>(par + i));
-            const float2 z = __half22float2(*reinterpret_cast<const __half2*>(par + pairs + i));
-            const float x = fmaf(levels, s.x, fabsf(z.x)), y = fmaf(levels, s.y, fabsf(z.y));
-            top = fmaxf(top, fmaxf(x < INFINITY ? x : 0.0f, y < INFINITY ? y : 0.0f));
+        for (int i = lane; i < pairs; i += DT) {
+            const float x = fmaf(levels, __half2float(par[i]), fabsf(__half2float(par[pairs + i])));
+            top = fmaxf(top, x < INFINITY ? x : 0.0f);
         }
-        for (int i = tid; i < lo.K * pairs; i += DT) {
+        for (int i = lane; i < lo.K * pairs; i += DT) {
             const float x = fabsf(__uint_as_float(side[i] & 0xffff0000u));
             top = fmaxf(top, x < INFINITY ? x : 0.0f);
         }
@@ -428,7 +454,7 @@ template <int D, int DT>
 __device__ __forceinline__ void fp8_keys(const uint8_t* codes, int cnt, bool e4m3, uint8_t* kt, int tid) {
     constexpr uint32_t sbo = D / 8 * kCoreBytes;
     for (int i = tid; i < 128 * D / 16; i += DT) {
-        const int row = (i & 7) + 8 * (i / (D / 2)), unit = (i >> 3) % (D / 16), tok = packed_token(row);
+        const int row = (i & 7) + 8 * (i / (D / 2)), unit = ((i >> 3) + row) % (D / 16), tok = packed_token(row);
         if ((row & ~15) >= cnt) break;
         uint32_t o[8];
         fp8_16(*reinterpret_cast<const uint4*>(codes + tok * D + 16 * unit), e4m3, o);
@@ -462,7 +488,7 @@ __device__ __forceinline__ void fp8_values(const uint8_t* codes, int cnt, bool e
 template <int D, int DT>
 __device__ __forceinline__ void rows_codes(const uint8_t* codes, int cnt, int kv, bool int8, uint8_t* tile, int tid) {
     for (int i = tid; i < 128 * D / 16; i += DT) {
-        const int row = (i & 7) + 8 * (i / (D / 2)), unit = (i >> 3) % (D / 16);
+        const int row = (i & 7) + 8 * (i / (D / 2)), unit = ((i >> 3) + row) % (D / 16);
         if ((row & ~15) >= cnt) break;
         uint32_t o[8] = {};
         if (row < cnt) {
@@ -603,7 +629,7 @@ __device__ __noinline__ void raw_rows(const TreeArgs& a, int b, int h, const Tre
                     *reinterpret_cast<uint4*>(at + 16 * kCoreBytes) = make_uint4(pw[4], pw[5], pw[6], pw[7]);
                 }
             }
-            if (lane < 8) {
+            if (lane < 8 && kf) {
                 if (kv)
                     vlog[row] = static_cast<float>(e);
                 else
@@ -643,47 +669,45 @@ __device__ __noinline__ void turn_keys(uint8_t* kt, const float* w, int64_t t0, 
     }
 }
 
+// What a kernel unpacks: KIVI records of 2, 4 or 8 bits, KIVI records read where they lie (any
+// bits; those that do not fit next to the operand tiles), INT8 and INT4 rows, FP8 tiles.  The
+// kinds are kernels of their own: together in one, their code costs every role registers.
+enum TreeKind { kKivi2 = 2, kKivi4 = 4, kKivi8 = 8, kInPlace = 16, kRows = 32, kFp8 = 64 };
+
 // Shapes of an instantiation: N columns, D channels.
 template <int N, int D>
 struct TreeShape {
-    static constexpr int kSoft = N >= 64 ? 8 : 4;               // softmax warps
-    static constexpr int kUnpack = N >= 64 ? 8 : 16;            // unpack warps
-    static constexpr int kThreads = 32 * (kSoft + kUnpack + 2);
-    static constexpr int NH = N / (kSoft / 4);                  // columns of a softmax thread
-    static constexpr bool kKeep = NH <= 32;                     // its scores stay in registers
-    static constexpr int B = kKeep ? NH : 16;                   // columns of one TMEM access
+    static constexpr int kThreads = N > 64 || (D > 128 && N > 16) ? 512 : 256;
+    static constexpr int kBlocks = N > 64 || D > 128 ? 1 : 2;   // of an SM
+    static constexpr int NH = N / (kThreads / 128);             // columns of a thread
+    static constexpr int B = NH;                                // of one TMEM access
     static constexpr int kDN = D > 128 ? 2 : 1;                 // accumulators of 128 channels
-    static constexpr int kTmem = N * (2 + kDN);                 // two score tiles and O^T
-    static constexpr uint32_t kCols = kTmem <= 64 ? 64 : kTmem <= 128 ? 128 : kTmem <= 256 ? 256 : 512;
+    static constexpr int kTmem = N * (1 + kDN);                 // the scores and O^T
+    static constexpr uint32_t kCols = kTmem <= 32 ? 32 : kTmem <= 64 ? 64 : kTmem <= 128 ? 128 : kTmem <= 256 ? 256 : 512;
     // shared memory: K, V (the product reads 128 channel rows of it), Q, P, then the stages
     static constexpr int kVBytes = D > 128 ? 65536 : 32768;
     static constexpr int kK = 0, kV = 256 * D, kQ = kV + kVBytes, kP = kQ + 2 * N * D, kStage = kP + 256 * N;
 };
 
-__device__ __forceinline__ void bar_sync(int id, int threads) {
-    asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-__device__ __forceinline__ bool bar_or(int id, int threads, bool p) {
+__device__ __forceinline__ bool elect_one() {
     uint32_t r;
-    asm volatile(
-        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, %3, p;\n selp.u32 %0, 1, 0, q;\n}"
-        : "=r"(r)
-        : "r"(static_cast<uint32_t>(p)), "r"(id), "r"(threads)
-        : "memory");
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
     return r != 0;
 }
-// Bounded wait by the SM's clock, about a second: the global timer's reads cost more than the
-// hand-over of a tile.
-__device__ __forceinline__ bool mbar_wait_clock(uint64_t* bar, uint32_t parity) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const long long t0 = clock64();
-    for (;;) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if (clock64() - t0 > 2000000000ll) return false;
+// Bounded wait of about a second.  The thread sleeps in the instruction (up to a millisecond at
+// a time): warps that poll take the issue slots and the shared-memory pipe of those that work.
+__device__ __forceinline__ bool mbar_wait_asleep(uint64_t* bar, uint32_t parity) {
+    const uint32_t at = smem_addr(bar);
+    for (int i = 0; i < 2000; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
+            : "=r"(ok)
+            : "r"(at), "r"(parity), "r"(1000000u)
+            : "memory");
+        if (ok) return true;
     }
-}
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+    return false;
 }
 // Two binary32 lanes at a time.
 __device__ __forceinline__ uint64_t pack2(float x, float y) {
@@ -716,7 +740,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 
 // A block's walk over its share of the tiles: segments, each the tiles [first, end) of one row
-// tile of one KV head.  Every role walks on its own.
+// tile of one KV head.
 struct TreeWalk {
     int b, h, rt, first, end, unit_tiles;
     bool live;
@@ -767,17 +791,25 @@ struct TreeWalk {
     }
 };
 
-// Everything the roles share next to the operand tiles.
+// What a block shares next to the operand tiles.
 template <int N, int D>
 struct TreeShared {
     float colg[N], colr[N];         // a column's query scale and minus its reference
     float fac[N], part[4][N];       // per column: factors; per quadrant: maxima, sums
-    float kf[2][128], vl[2][128];   // a token's score factor and log2 of its value scale
+    float kf[128], vl[128];         // a raw row's score factor and log2 of its value scale
     float wt[D / 2];                // rotary frequencies in the order of the key tile
     int64_t scan[32], start[2];
-    uint64_t stage_full[2], stage_empty[2], k_full, k_empty, v_full, pv_done, s_full[2], s_empty[2], p_full, q_full, done;
-    const uint8_t* recs[2][8];
+    uint64_t stage_full[2], s_full, pv_done;
+    const uint8_t* recs[8];         // records read in place
+    int qtop, qlow;                 // exponents of the largest and the smallest query
     uint32_t tmem, top[2];
+    TreeWalk walk;                  // the segment
+    int more;
+    // the next packed tile to bring in: its segment, the unit's packed bytes and groups
+    TreeWalk ahead;
+    const uint8_t* ahead_base;
+    int ahead_tile, ahead_end, ahead_groups;
+    uint32_t ahead_slot;
     int dead, odd;                  // a wait gave up; a draft's value is not finite
 };
 
@@ -797,36 +829,262 @@ __device__ __forceinline__ float warp_max(float x) {
     return r;
 }
 
+// The queries of a segment's columns into their tile: a warp takes an octet of columns, a lane
+// 16 channels at a time.  All are stored under the largest one's power of two; a query 2^20
+// below it keeps binary16's subnormal steps, 2^-39 of the largest.  Where one is smaller
+// still, each gets a power of its own, and the scores their columns' factors.  Returns (such
+// factors are needed, the factor of all scores); ends behind a block barrier.
 template <int N, int D>
-__global__ void __launch_bounds__(TreeShape<N, D>::kThreads, 1) k_tree(const __grid_constant__ TreeArgs a) {
+__device__ __noinline__ float2 load_queries(const TreeArgs& a, int row0, int row_end, int W, uint8_t* qt,
+                                            TreeShared<N, D>& sh) {
+    const TreeWalk& w = sh.walk;
+    constexpr int UNITS = D / 16, STEPS = (UNITS + 3) / 4, WARPS = TreeShape<N, D>::kThreads / 32;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gqa = a.lo.gqa;
+    if (tid == 0) {
+        sh.qtop = -200;
+        sh.qlow = 200;
+    }
+    __syncthreads();
+    auto query = [&](int o, uint32_t (&q)[STEPS][8]) {
+        const int r = row0 + 8 * o + (lane & 7);
+        const uint16_t* p = nullptr;
+        if (r < row_end)
+            p = reinterpret_cast<const uint16_t*>(a.q) +
+                (((int64_t)w.b * a.nodes + (r >> a.gshift)) * a.lo.Hq + w.h * gqa + (r & (gqa - 1))) * D;
+        float mx = 0.0f;
+        bool odd = false;
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) {
+            const int unit = (lane >> 3) + 4 * i;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) q[i][j] = 0u;
+            if (p && unit < UNITS) load_words(p + 16 * unit, q[i]);
+            mx = fmaxf(mx, unit_top(q[i], &odd));
+        }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+        return fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+    };
+    for (int o = warp; o < N / 8; o += WARPS) {
+        uint32_t q[STEPS][8];
+        const float mx = query(o, q);
+        if (lane < 8 && mx > 0.0f) {
+            atomicMax(&sh.qtop, range_exponent(mx));
+            atomicMin(&sh.qlow, range_exponent(mx));
+        }
+    }
+    __syncthreads();
+    const bool mixed = sh.qtop - sh.qlow > 20;
+    const int common = sh.qtop > -200 ? sh.qtop : 0;
+    for (int o = warp; o < N / 8; o += WARPS) {
+        uint32_t q[STEPS][8];
+        const float mx = query(o, q);
+        const int c = 8 * o + (lane & 7), e = mixed ? range_exponent(mx) : common;
+        const float f = pow2i(-e);
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) {
+            const int unit = (lane >> 3) + 4 * i;
+            if (unit >= UNITS) continue;
+            uint32_t hw[8];
+            half_words(q[i], f, false, hw);
+            store_unit<D>(qt, c, unit, hw, W);
+        }
+        if (lane < 8) {
+            sh.colg[c] = a.qscale * pow2i(e);
+            sh.colr[c] = -kNoMax;
+        }
+    }
+    __syncthreads();
+    return make_float2(mixed ? 1.0f : 0.0f, mixed ? 1.0f : a.qscale * pow2i(common));
+}
+
+// The result of a segment: O^T (TMEM, from `tm` on for this warp's lanes and columns) over the
+// columns' sums (sh.part), as bf16 outputs where the segment is a whole row tile, else as a
+// partial result (m, l, O).
+template <int N, int D, bool ROWS>
+__device__ __noinline__ void finish_segment(const TreeArgs& a, int first, uint32_t tm, int row0, int row_end,
+                                            int W, TreeShared<N, D>& sh) {
     using S = TreeShape<N, D>;
-    constexpr int NT = S::kThreads, ST = 32 * S::kSoft, DT = 32 * S::kUnpack;
+    const Layout& lo = a.lo;
+    const TreeWalk& w = sh.walk;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = warp & 3, col0 = (warp >> 2) * S::NH;
+    const bool whole = first == 0 && w.end == w.unit_tiles;
+    const int64_t slot = blockIdx.x + ((int64_t)w.b * lo.H + w.h) * a.RT + w.rt;
+    for (int c = tid; c < N; c += S::kThreads) {
+        // rows of padding nodes saw the cached tokens with a query of 0: their output is 0
+        const float v = w.live && row0 + c < row_end ? (sh.part[0][c] + sh.part[1][c]) + (sh.part[2][c] + sh.part[3][c]) : 0.0f;
+        if (whole) {
+            sh.fac[c] = v != 0.0f ? 1.0f / v : 0.0f;
+        } else {
+            sh.fac[c] = v != 0.0f ? 1.0f : 0.0f;
+            reinterpret_cast<float2*>(a.ws + a.ml_off)[slot * N + c] = make_float2(-sh.colr[c], v);
+        }
+    }
+    __syncthreads();
+    const bool odd = sh.odd != 0;
+#pragma unroll 1
+    for (int d = 0; d < S::kDN; ++d) {
+        const int ch0 = 128 * d + 32 * quad;
+        if (ch0 >= D) continue;
+        // lane -> channel: the order of the tile's value rows
+        const int ch = ROWS ? place_channel(ch0 + lane, W, D) : ch0 + lane;
+#pragma unroll 1
+        for (int c0 = 0; c0 < S::NH; c0 += 8) {
+            float o[8];
+            if (w.live) tmem_load(tm + d * N + c0, o);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int c = col0 + c0 + i, r = row0 + c;
+                if (r >= a.rows) continue;
+                const float fc = sh.fac[c];
+                float v = fc != 0.0f ? o[i] * fc : 0.0f;
+                if (odd && r < row_end) {   // drafts whose value is not finite, in the rows that see them
+                    const int node = r >> a.gshift;
+                    for (int j = 0; j < w.s.nodes; ++j) {
+                        const float y = __bfloat162float(a.v[(((int64_t)w.b * a.nodes + j) * lo.H + w.h) * D + ch]);
+                        if (fabsf(y) < INFINITY) continue;
+                        if (a.mask ? a.mask[((int64_t)w.b * a.nodes + node) * a.nodes + j] != 0 : j <= node) v += y;
+                    }
+                }
+                if (whole)
+                    a.out[(((int64_t)w.b * a.nodes + (r >> a.gshift)) * lo.Hq + w.h * lo.gqa + (r & (lo.gqa - 1))) * D + ch] =
+                        __float2bfloat16_rn(v);
+                else
+                    reinterpret_cast<float*>(a.ws + a.o_off)[(slot * N + c) * D + ch] = v;
+            }
+        }
+    }
+}
+
+// A KIVI key tile's further steps: the scaled tile (scaled: always, else where ke != 0), the
+// outliers, the rotation; behind and before block barriers.
+template <int D, int DT, typename Tile>
+__device__ __noinline__ void kivi_keys_rest(const TreeArgs& a, const Tile t, uint8_t* kt, const float* wt, int64_t t0, int ke,
+                                            bool scaled, int W, int tid) {
+    if (ke != 0 || scaled) {
+        kivi_keys_scaled<D, DT>(a.lo, t, kt, pow2i(-ke), W, tid);
+        __syncthreads();
+    }
+    if (a.lo.K > 0) {
+        kivi_outliers<D, DT>(a.lo, t, kt, 0, pow2i(-ke), W, tid);
+        __syncthreads();
+    }
+    if (a.lo.rope_base > 0.0f) turn_keys<D, DT>(kt, wt, t0, t.cnt, true, tid);
+}
+// The exponents of the keys and values of a tile that may reach outside binary16 (0: they do
+// not); behind and before block barriers.
+template <int DT, typename Tile>
+__device__ __noinline__ void kivi_exponents(const Layout& lo, const Tile t, uint32_t* top, int* ke, int* ve, int tid) {
+    if (tid < 2) top[tid] = 0u;
+    __syncthreads();
+    for (int kv = 0; kv < 2; ++kv) atomicMax(&top[kv], __float_as_uint(kivi_bound<DT>(lo, t, kv, tid)));
+    __syncthreads();
+    const float k = __uint_as_float(top[0]), v = __uint_as_float(top[1]);
+    *ke = k >= 32768.0f ? range_exponent(k) : 0;
+    *ve = v >= 32768.0f ? range_exponent(v) : 0;
+    __syncthreads();
+}
+
+// The unit that sh.ahead is in, for copy_next; to the next unit with packed tiles where it has
+// none left (`on`).  One thread.
+template <int N, int D>
+__device__ __noinline__ void copy_unit(const TreeArgs& a, TreeShared<N, D>& sh, bool on) {
+    TreeWalk& w = sh.ahead;
+    for (;;) {
+        if (on && !w.next(a, N)) {
+            sh.ahead_tile = sh.ahead_end = 0;
+            w.left = 0;
+            return;
+        }
+        on = true;
+        const int end = w.live ? (w.end < w.s.packed ? w.end : w.s.packed) : 0;
+        if (w.first >= end) continue;
+        sh.ahead_tile = w.first;
+        sh.ahead_end = end;
+        sh.ahead_groups = a.TG > 0 ? w.s.qn / a.lo.G : 0;
+        sh.ahead_base = a.cache + a.lo.data_off + unit_index(a.lo, a.layer, w.b, w.h) * a.lo.unit;
+        return;
+    }
+}
+// Brings the block's next packed tile, if there is one, to the next stage; one thread.
+template <int N, int D, int KIND>
+__device__ __forceinline__ void copy_next(const TreeArgs& a, TreeShared<N, D>& sh, uint8_t* stage) {
+    constexpr bool rows_scheme = KIND == kRows;
+    const Layout& lo = a.lo;
+    if (sh.ahead_tile >= sh.ahead_end) {
+        if (sh.ahead.left <= 0) return;
+        copy_unit(a, sh, true);
+        if (sh.ahead_tile >= sh.ahead_end) return;
+    }
+    if (*static_cast<volatile int*>(&sh.dead)) return;
+    const int tile = sh.ahead_tile;
+    const uint32_t slot = sh.ahead_slot;
+    sh.ahead_tile = tile + 1;
+    if (a.stages == 2) sh.ahead_slot = slot ^ 1;
+    uint8_t* to = stage + slot * a.stage_bytes;
+    uint64_t* bar = &sh.stage_full[slot];
+    if constexpr (KIND <= kInPlace) {
+        const int g0 = tile * a.TG, rest = sh.ahead_groups - g0, ng = rest < a.TG ? rest : a.TG;
+        mbar_arrive_expect_tx(bar, static_cast<uint32_t>(ng * lo.rec));
+        if (lo.PG == 0) {
+            bulk_copy_g2s(to, sh.ahead_base + (int64_t)g0 * lo.rec, ng * lo.rec, bar);
+        } else {
+            const TreeWalk& w = sh.ahead;
+            const int32_t* table = lo.table + (int64_t)w.b * lo.MP;
+            int pg = g0 / lo.PG, in = g0 - pg * lo.PG;
+            for (int g = 0; g < ng; ++g) {
+                int32_t page = table[pg];
+                if (page < 0 || page >= lo.NP) {        // outside the pool: page 0 in its place, reported
+                    atomicOr(reinterpret_cast<uint32_t*>(a.ws), KVQ_STATUS_BAD_PAGE);
+                    page = 0;
+                }
+                bulk_copy_g2s(to + g * lo.rec,
+                              a.cache + lo.data_off + (int64_t)page * lo.page + (((int64_t)a.layer * lo.H + w.h) * lo.PG + in) * lo.rec,
+                              lo.rec, bar);
+                if (++in == lo.PG) {
+                    in = 0;
+                    ++pg;
+                }
+            }
+        }
+    } else {
+        const int row_bytes = lo.scheme == KVQ_SCHEME_INT4 ? D / 2 : D;
+        const int cnt = sh.ahead.packed_count(a, tile), c16 = (cnt + 15) & ~15;
+        const uint8_t* src = sh.ahead_base + (int64_t)tile * (128 * row_bytes);
+        const uint32_t bytes = static_cast<uint32_t>(c16 * row_bytes);
+        mbar_arrive_expect_tx(bar, 2 * bytes + (rows_scheme ? 8 * c16 : 0));
+        bulk_copy_g2s(to, src, bytes, bar);
+        bulk_copy_g2s(to + 128 * row_bytes, src + (int64_t)lo.T16 * row_bytes, bytes, bar);
+        if (rows_scheme) {
+            const uint8_t* sc = sh.ahead_base + 2 * (int64_t)lo.T16 * row_bytes + 512 * (int64_t)tile;
+            bulk_copy_g2s(to + 256 * row_bytes, sc, 4 * c16, bar);
+            bulk_copy_g2s(to + 256 * row_bytes + 512, sc + 4 * (int64_t)lo.T16, 4 * c16, bar);
+        }
+    }
+}
+
+template <int N, int D, int KIND>
+__global__ void __launch_bounds__(TreeShape<N, D>::kThreads, TreeShape<N, D>::kBlocks) k_tree(const __grid_constant__ TreeArgs a) {
+    using S = TreeShape<N, D>;
+    constexpr int NT = S::kThreads, CT = S::kThreads, NH = S::NH, B = S::B;
+    constexpr bool kivi = KIND <= kInPlace, staged_tiles = KIND != kInPlace, fp8 = KIND == kFp8, rows_scheme = KIND == kRows;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ __align__(16) TreeShared<N, D> sh;
 
     const Layout& lo = a.lo;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, quad = warp & 3, col0 = (warp >> 2) * NH;
+    const int row = 32 * quad + lane;                                   // this thread's token of a tile
+    const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
     const int H = lo.H, gqa = lo.gqa, W = key_block(lo);
     uint8_t *kt = smem + S::kK, *vt = smem + S::kV, *qt = smem + S::kQ, *pt = smem + S::kP, *stage = smem + S::kStage;
-    const bool kivi = lo.scheme == KVQ_SCHEME_KIVI, fp8 = is_fp8(lo.scheme), rows_scheme = is_rows(lo.scheme);
-    const bool rope = lo.rope_base > 0.0f;
+    const bool rope = kivi && lo.rope_base > 0.0f;
     const int row_bytes = lo.scheme == KVQ_SCHEME_INT4 ? D / 2 : D;     // of a code row
 
     if (warp == 0) tmem_alloc(&sh.tmem, S::kCols);
     if (tid == 32) {
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&sh.stage_full[i], 1);
-            mbar_init(&sh.stage_empty[i], S::kUnpack);
-            mbar_init(&sh.s_full[i], 2);
-            mbar_init(&sh.s_empty[i], S::kSoft);
-        }
-        mbar_init(&sh.k_full, S::kUnpack);
-        mbar_init(&sh.k_empty, 1);
-        mbar_init(&sh.v_full, S::kUnpack);
+        mbar_init(&sh.stage_full[0], 1);
+        mbar_init(&sh.stage_full[1], 1);
+        mbar_init(&sh.s_full, 1);
         mbar_init(&sh.pv_done, 1);
-        mbar_init(&sh.p_full, S::kSoft);
-        mbar_init(&sh.q_full, S::kSoft);
-        mbar_init(&sh.done, 1);
         sh.dead = 0;
         sh.odd = 0;
     }
@@ -856,165 +1114,231 @@ __global__ void __launch_bounds__(TreeShape<N, D>::kThreads, 1) k_tree(const __g
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
-    const uint32_t tm_s = sh.tmem, tm_o = tm_s + 2 * N;
+    const uint32_t tm_s = sh.tmem, tm_o = tm_s + N, my_s = tm_s + lanes + col0;
 
-    auto dead = [&]() { return *static_cast<volatile int*>(&sh.dead) != 0; };
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (dead()) return;
-        if (!mbar_wait_clock(bar, parity & 1)) {
+        if (*static_cast<volatile int*>(&sh.dead)) return;
+        if (!mbar_wait_asleep(bar, parity & 1)) {
             sh.dead = 1;
             atomicOr(reinterpret_cast<uint32_t*>(a.ws), KVQ_STATUS_TIMEOUT);
         }
     };
-    // a warp's shared-memory writes, ready for the products
-    auto publish = [&](uint64_t* bar) {
-        smem_to_async();
-        tmem_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar);
-    };
-
+    // the stage that the i-th packed tile of this block passes through, and how often it did
+    auto slot_of = [&](uint32_t i) { return a.stages == 2 ? i & 1 : 0u; };
+    auto turn_of = [&](uint32_t i) { return a.stages == 2 ? i >> 1 : i; };
     if (static_cast<int64_t>(blockIdx.x) < nb) {
-        TreeWalk w;
-        w.begin(a, N, static_cast<int>(sh.start[0]), sh.start[1], x1 - x0);
-        if (warp < S::kSoft) {
-            // ======================================================================= softmax
-            const int quad = warp & 3, half = warp >> 2, row = 32 * quad + lane, col0 = half * S::NH;
-            const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
-            uint32_t it = 0;
-            do {
-                const int row0 = w.rt * N, row_end = w.s.nodes << a.gshift;
-                float l[S::NH];
+        // the walk is kept in shared memory: its fields are needed now and then, and a register
+        // that does not hold one of them saves a trip to local memory
+        TreeWalk& w = sh.walk;
+        if (tid == 0) {
+            w.begin(a, N, static_cast<int>(sh.start[0]), sh.start[1], x1 - x0);
+            if (staged_tiles) {
+                sh.ahead = w;
+                sh.ahead_slot = 0;
+                copy_unit(a, sh, false);
+                for (int i = 0; i < a.stages; ++i) copy_next<N, D, KIND>(a, sh, stage);
+            }
+        }
+        __syncthreads();
+        uint32_t it = 0, used = 0;              // tiles, and packed tiles, so far
+        do {
+            const int row0 = w.rt * N, row_end = w.s.nodes << a.gshift, first = w.first, end = w.end, packed_end = w.s.packed;
+            const bool live = w.live;
+            bool mixed = false;
+            float gscale = 1.0f;
+            float l[NH];
 #pragma unroll
-                for (int i = 0; i < S::NH; ++i) l[i] = 0.0f;
-                if (w.live) {
-                    // queries: a warp takes an octet of columns, a lane 16 channels at a time
-                    constexpr int UNITS = D / 16, STEPS = (UNITS + 3) / 4;
-                    for (int o = warp; o < N / 8; o += S::kSoft) {
-                        const int c = 8 * o + (lane & 7), r = row0 + c;
-                        const uint16_t* p = nullptr;
-                        if (r < row_end)
-                            p = reinterpret_cast<const uint16_t*>(a.q) +
-                                (((int64_t)w.b * a.nodes + (r >> a.gshift)) * lo.Hq + w.h * gqa + (r & (gqa - 1))) * D;
-                        uint32_t q[STEPS][8];
-                        float mx = 0.0f;
-                        bool odd = false;
-#pragma unroll
-                        for (int i = 0; i < STEPS; ++i) {
-                            const int unit = (lane >> 3) + 4 * i;
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) q[i][j] = 0u;
-                            if (p && unit < UNITS) load_words(p + 16 * unit, q[i]);
-                            mx = fmaxf(mx, unit_top(q[i], &odd));
+            for (int i = 0; i < NH; ++i) l[i] = 0.0f;
+            if (live) {
+                const float2 m = load_queries<N, D>(a, row0, row_end, W, qt, sh);
+                mixed = m.x != 0.0f;
+                gscale = m.y;
+            }
+            for (int tile = first; live && tile < end; ++tile, ++it) {
+                const bool packed = tile < packed_end;
+                const int cnt = packed ? w.packed_count(a, tile) : w.raw_count(tile);
+                int ke = 0, ve = 0;                                     // KIVI: exponents outside binary16
+                const uint32_t slot = slot_of(used);
+                const uint8_t* raw = stage + slot * a.stage_bytes;
+                PackedTile<staged_tiles> t;
+                t.base = raw;
+                t.stride = lo.rec;
+                t.recs = sh.recs;
+                t.cnt = cnt;
+                // ---- keys (the scores of the tile before are out of TMEM: its votes are behind a barrier)
+                if (!packed) {
+                    const int r0 = (tile - w.s.packed) * 128, held = w.s.n - w.s.qn - r0;
+                    wait(&sh.pv_done, it + 1);                          // the rows write both tiles
+                    raw_rows<D, CT>(a, w.b, w.h, w.s, r0, cnt, W, rows_scheme, kt, nullptr, sh.kf, sh.vl, &sh.odd, 0, tid);
+                    raw_rows<D, CT>(a, w.b, w.h, w.s, r0, cnt, W, rows_scheme, nullptr, vt, sh.kf, sh.vl, &sh.odd, 1, tid);
+                    if (rope) {
+                        __syncthreads();
+                        turn_keys<D, CT>(kt, sh.wt, (int64_t)w.s.qn + r0, held < cnt ? held : cnt, false, tid);
+                    }
+                    smem_to_async();
+                    tmem_fence_before();
+                    __syncthreads();
+                } else {
+                    if constexpr (staged_tiles) {
+                        wait(&sh.stage_full[slot], turn_of(used));
+                    } else {
+                        // records too large to pass through shared memory next to the tiles
+                        if (tid < 8 && tid * lo.G < cnt) {
+                            int64_t off = group_offset(lo, a.layer, w.b, w.h, (int64_t)tile * a.TG + tid);
+                            if (off < 0) {
+                                atomicOr(reinterpret_cast<uint32_t*>(a.ws), KVQ_STATUS_BAD_PAGE);
+                                off = lo.data_off + (((int64_t)a.layer * H + w.h) * lo.PG + (tile * a.TG + tid) % lo.PG) * lo.rec;
+                            }
+                            sh.recs[tid] = a.cache + off;
                         }
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                        const int e = range_exponent(mx);
-                        const float f = pow2i(-e);
-#pragma unroll
-                        for (int i = 0; i < STEPS; ++i) {
-                            const int unit = (lane >> 3) + 4 * i;
-                            if (unit >= UNITS) continue;
-                            uint32_t hw[8];
-                            half_words(q[i], f, false, hw);
-                            store_unit<D>(qt, c, unit, hw, W);
+                        __syncthreads();
+                    }
+                    ++used;
+                    bool wide = false;
+                    if constexpr (kivi) {
+                        wide = kivi_wide<CT>(a, t, tid);
+                        if constexpr (KIND <= kKivi8) kivi_keys<D, KIND, CT>(a, t, kt, tid);
+                        if (lo.K > 0 || rope || KIND == kInPlace) {
+                            if (__syncthreads_or(wide)) kivi_exponents<CT>(lo, t, sh.top, &ke, &ve, tid);
+                            kivi_keys_rest<D, CT>(a, t, kt, sh.wt, (int64_t)tile * a.TT, ke, KIND == kInPlace, W, tid);
+                            wide = false;
                         }
-                        if (lane < 8) {
-                            sh.colg[c] = a.qscale * pow2i(e);
-                            sh.colr[c] = -kNoMax;
+                    } else {
+                        if constexpr (fp8) fp8_keys<D, CT>(raw, cnt, lo.scheme == KVQ_SCHEME_FP8_E4M3, kt, tid);
+                        else rows_codes<D, CT>(raw, cnt, 0, lo.scheme == KVQ_SCHEME_INT8, kt, tid);
+                    }
+                    smem_to_async();
+                    tmem_fence_before();
+                    if (__syncthreads_or(wide)) {
+                        if constexpr (kivi) {   // some value may be outside binary16: the tile again, scaled
+                            kivi_exponents<CT>(lo, t, sh.top, &ke, &ve, tid);
+                            if (ke != 0) kivi_keys_rest<D, CT>(a, t, kt, sh.wt, (int64_t)tile * a.TT, ke, false, W, tid);
+                            smem_to_async();
+                            __syncthreads();
                         }
                     }
-                    publish(&sh.q_full);
-                    bar_sync(2, ST);
                 }
-                const int first = w.first;
-                for (int tile = first; w.live && tile < w.end; ++tile, ++it) {
-                    const bool packed = tile < w.s.packed;
-                    const int cnt = packed ? w.packed_count(a, tile) : w.raw_count(tile);
-                    const int tok = packed && !rows_scheme ? packed_token(row) : row;
-                    const bool valid = tok < cnt, masked = cnt < 128 || !packed;
-                    int draft = -1;
-                    if (!packed && valid) draft = (tile - w.s.packed) * 128 + row - (w.s.n - w.s.qn);
-                    const uint32_t my_s = tm_s + (it & 1) * N + lanes + col0;
-                    wait(&sh.s_full[it & 1], it >> 1);
+                if (warp == 0 && elect_one()) {
                     tmem_fence_after();
-                    const float f = valid ? sh.kf[it & 1][row] : 0.0f, lv = valid ? sh.vl[it & 1][row] : 0.0f;
-                    const float inv = tree_exp2(-lv);
-                    const uint64_t f2 = pack2(f, f), lv2 = pack2(lv, lv), inv2 = pack2(inv, inv);
-                    // x + log2 s of B columns from c0 on, less the references if REF
-                    auto scores = [&](int c0, float (&x)[S::B], bool ref) {
-                        tmem_load(my_s + c0, x);
+                    const uint64_t dk = mma_desc(smem_addr(kt), D / 8 * kCoreBytes), dq = mma_desc(smem_addr(qt), D / 8 * kCoreBytes);
 #pragma unroll
-                        for (int i = 0; i < S::B; i += 4) {
-                            const ulonglong2 g = *reinterpret_cast<const ulonglong2*>(&sh.colg[col0 + c0 + i]);
-                            uint64_t u = fma2(pack2(x[i], x[i + 1]), mul2(f2, g.x), lv2);
-                            uint64_t v = fma2(pack2(x[i + 2], x[i + 3]), mul2(f2, g.y), lv2);
-                            if (ref) {
-                                const ulonglong2 r = *reinterpret_cast<const ulonglong2*>(&sh.colr[col0 + c0 + i]);
-                                u = add2(u, r.x);
-                                v = add2(v, r.y);
-                            }
-                            unpack2(u, &x[i], &x[i + 1]);
-                            unpack2(v, &x[i + 2], &x[i + 3]);
-                        }
-                        if (masked) {
-#pragma unroll
-                            for (int i = 0; i < S::B; ++i) {
-                                bool see = valid;
-                                if (draft >= 0) {
-                                    const int r = row0 + col0 + c0 + i, node = r >> a.gshift;
-                                    see = r < row_end && (a.mask ? a.mask[((int64_t)w.b * a.nodes + node) * a.nodes + draft] != 0
-                                                                 : draft <= node);
-                                }
-                                x[i] = see ? x[i] : -INFINITY;
-                            }
-                        }
-                    };
-                    float x[S::B];
-                    float hi = kNoMax;
-#pragma unroll
-                    for (int c0 = 0; c0 < S::NH; c0 += S::B) {
-                        scores(c0, x, true);
-#pragma unroll
-                        for (int i = 0; i < S::B; i += 2) hi = max3(hi, x[i], x[i + 1]);
+                    for (int k = 0; k < D / 16; ++k)
+                        mma_f16(tm_s, dk + k * (2 * kCoreBytes >> 4), dq + k * (2 * kCoreBytes >> 4),
+                                mma_idesc(128, N, false, false), k > 0);
+                    mma_commit(&sh.s_full);
+                }
+                __syncwarp();
+                // ---- this thread's token: factor of its scores, log2 of its values' scale
+                const int tok = packed && !rows_scheme ? packed_token(row) : row;
+                const bool valid = tok < cnt, masked = cnt < 128 || !packed;
+                int draft = -1;
+                float f = 0.0f, lv = 0.0f;
+                if (valid) {
+                    if (!packed) {
+                        f = sh.kf[row];
+                        lv = sh.vl[row];
+                        draft = (tile - w.s.packed) * 128 + row - (w.s.n - w.s.qn);
+                    } else if constexpr (kivi) {
+                        f = pow2i(ke);
+                        lv = static_cast<float>(ve);
+                    } else if constexpr (fp8) {
+                        f = fp8_scale(a, w.h)[0];
+                        lv = fmaxf(fast_log2(fabsf(fp8_scale(a, w.h)[1])), -110.0f);
+                    } else {
+                        const float* sc = reinterpret_cast<const float*>(raw + 256 * row_bytes);
+                        f = sc[tok];
+                        lv = fmaxf(fast_log2(sc[128 + tok]), -110.0f);  // (a scale of 0 belongs to codes of 0)
                     }
-                    const bool over = bar_or(2, ST, hi > kReach);
-                    if (over) {
-                        // the columns' maxima over the tile, the new references, and everything so
-                        // far under them
-#pragma unroll 1
-                        for (int c0 = 0; c0 < S::NH; c0 += S::B) {
-                            scores(c0, x, false);
+                    f *= gscale;
+                }
+                // ---- values, while the scores are computed
+                if (packed) {
+                    wait(&sh.pv_done, it + 1);                          // the tile before has been read
+                    if constexpr (kivi) {
+                        if (ve != 0 || KIND == kInPlace) {
+                            kivi_values_scaled<D, CT>(lo, t, vt, pow2i(-ve), tid);
+                        } else if constexpr (KIND <= kKivi8) {
+                            kivi_values<D, KIND, CT>(a, t, vt, tid);
+                        }
+                        if (lo.K > 0) {
+                            __syncthreads();
+                            kivi_outliers<D, CT>(lo, t, vt, 1, pow2i(-ve), W, tid);
+                        }
+                    } else {
+                        const uint8_t* vraw = raw + 128 * row_bytes;
+                        if constexpr (fp8) fp8_values<D, CT>(vraw, cnt, lo.scheme == KVQ_SCHEME_FP8_E4M3, fp8_scale(a, w.h)[1] < 0.0f, vt, tid);
+                        else rows_codes<D, CT>(vraw, cnt, 1, lo.scheme == KVQ_SCHEME_INT8, vt, tid);
+                    }
+                }
+                // ---- softmax
+                const float inv = tree_exp2(-lv);
+                const uint64_t f2 = pack2(f, f), lv2 = pack2(lv, lv), inv2 = pack2(inv, inv);
+                // x + log2 s of B columns from c0 on, less the references if REF
+                auto scores = [&](int c0, float (&x)[B], bool ref) {
+                    tmem_load(my_s + c0, x);
+                    if (mixed) {
 #pragma unroll
-                            for (int i = 0; i < S::B; ++i) {
-                                const float m = warp_max(x[i]);
-                                if (lane == 0) sh.part[quad][col0 + c0 + i] = m;
+                        for (int i = 0; i < B; ++i) x[i] *= sh.colg[col0 + c0 + i];
+                    }
+#pragma unroll
+                    for (int i = 0; i < B; i += 4) {
+                        uint64_t u = fma2(pack2(x[i], x[i + 1]), f2, lv2), v = fma2(pack2(x[i + 2], x[i + 3]), f2, lv2);
+                        if (ref) {
+                            const ulonglong2 r = *reinterpret_cast<const ulonglong2*>(&sh.colr[col0 + c0 + i]);
+                            u = add2(u, r.x);
+                            v = add2(v, r.y);
+                        }
+                        unpack2(u, &x[i], &x[i + 1]);
+                        unpack2(v, &x[i + 2], &x[i + 3]);
+                    }
+                    if (masked) {
+#pragma unroll
+                        for (int i = 0; i < B; ++i) {
+                            bool see = valid;
+                            if (draft >= 0) {
+                                const int r = row0 + col0 + c0 + i, node = r >> a.gshift;
+                                see = r < row_end && (a.mask ? a.mask[((int64_t)w.b * a.nodes + node) * a.nodes + draft] != 0
+                                                             : draft <= node);
                             }
+                            x[i] = see ? x[i] : -INFINITY;
                         }
-                        bar_sync(2, ST);
-                        for (int c = tid; c < N; c += ST) {
-                            const float m = fmaxf(fmaxf(sh.part[0][c], sh.part[1][c]), fmaxf(sh.part[2][c], sh.part[3][c])) - kHead;
-                            const float old = -sh.colr[c], now = fmaxf(old, m);
-                            sh.colr[c] = -now;
-                            sh.fac[c] = tree_exp2(old - now);
-                        }
-                        bar_sync(2, ST);
-                        if (S::kKeep) scores(0, x, true);
                     }
-                    if (S::kKeep) {                     // the scores are out of TMEM
-                        tmem_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&sh.s_empty[it & 1]);
-                    }
-                    wait(&sh.pv_done, it + 1);          // of the tile before: P is free, O^T at rest
-                    tmem_fence_after();
-                    if (over && tile > first) {
+                };
+                wait(&sh.s_full, it);
+                tmem_fence_after();
+                float x[B];
+                float hi = kNoMax;
+                scores(0, x, true);
 #pragma unroll
-                        for (int i = 0; i < S::NH; ++i) l[i] *= sh.fac[col0 + i];
+                for (int i = 0; i < B; i += 2) hi = max3(hi, x[i], x[i + 1]);
+                const bool over = __syncthreads_or(hi > kReach);
+                // behind the barrier the tile's packed bytes are read: the next ones may come
+                if (staged_tiles && packed && warp == CT / 32 - 1 && elect_one()) copy_next<N, D, KIND>(a, sh, stage);
+                if (over) {
+                    // the columns' maxima over the tile, the new references, and everything so far
+                    // under them
+                    scores(0, x, false);
+#pragma unroll
+                    for (int i = 0; i < B; ++i) {
+                        const float m = warp_max(x[i]);
+                        if (lane == 0) sh.part[quad][col0 + i] = m;
+                    }
+                    __syncthreads();
+                    for (int c = tid; c < N; c += CT) {
+                        const float m = fmaxf(fmaxf(sh.part[0][c], sh.part[1][c]), fmaxf(sh.part[2][c], sh.part[3][c])) - kHead;
+                        const float old = -sh.colr[c], now = fmaxf(old, m);
+                        sh.colr[c] = -now;
+                        sh.fac[c] = tree_exp2(old - now);
+                    }
+                    __syncthreads();
+                    scores(0, x, true);
+                    if (tile > first) {
+#pragma unroll
+                        for (int i = 0; i < NH; ++i) l[i] *= sh.fac[col0 + i];
 #pragma unroll 1
                         for (int d = 0; d < S::kDN; ++d)
 #pragma unroll 1
-                            for (int c0 = 0; c0 < S::NH; c0 += 8) {
+                            for (int c0 = 0; c0 < NH; c0 += 8) {
                                 float o[8];
                                 const uint32_t at = tm_o + d * N + lanes + col0 + c0;
                                 tmem_load(at, o);
@@ -1023,319 +1347,63 @@ __global__ void __launch_bounds__(TreeShape<N, D>::kThreads, 1) k_tree(const __g
                                 tmem_store(at, o);
                             }
                     }
-                    uint8_t* prow = pt + (row >> 3) * kCoreBytes + (row & 7) * 16;
-#pragma unroll
-                    for (int c0 = 0; c0 < S::NH; c0 += S::B) {
-                        if (!S::kKeep) scores(c0, x, true);
-#pragma unroll
-                        for (int c = 0; c < S::B; c += 8) {
-                            uint32_t p[4];
-#pragma unroll
-                            for (int i = 0; i < 8; i += 2) {
-                                const float p0 = tree_exp2(x[c + i]), p1 = tree_exp2(x[c + i + 1]);
-                                float& l0 = l[c0 + c + i];
-                                float& l1 = l[c0 + c + i + 1];
-                                unpack2(fma2(pack2(p0, p1), inv2, pack2(l0, l1)), &l0, &l1);
-                                p[i / 2] = h2_as_u32(__floats2half2_rn(p0, p1));
-                            }
-                            *reinterpret_cast<uint4*>(prow + ((col0 + c0 + c) >> 3) * (16 * kCoreBytes)) =
-                                make_uint4(p[0], p[1], p[2], p[3]);
-                        }
-                    }
-                    if (!S::kKeep) {
-                        tmem_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&sh.s_empty[it & 1]);
-                    }
-                    publish(&sh.p_full);
                 }
-                // ------------------------------------------------------ the segment's result
-                const bool whole = first == 0 && w.end == w.unit_tiles;
-                const int64_t unit = ((int64_t)w.b * H + w.h) * a.RT + w.rt;
-                const int64_t slot = blockIdx.x + unit;
-                if (w.live) wait(&sh.pv_done, it + 1);
-                tmem_fence_after();
-                // the sums over a column's tokens
+                uint8_t* prow = pt + (row >> 3) * kCoreBytes + (row & 7) * 16;
 #pragma unroll
-                for (int i = 0; i < S::NH; ++i) {
-                    float v = l[i];
+                for (int c = 0; c < B; c += 8) {
+                    uint32_t p[4];
 #pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-                    if (lane == 0) sh.part[quad][col0 + i] = v;
-                }
-                bar_sync(2, ST);
-                for (int c = tid; c < N; c += ST) {
-                    // rows of padding nodes saw the cached tokens with a query of 0: their output is 0
-                    const float v = w.live && row0 + c < row_end
-                                        ? (sh.part[0][c] + sh.part[1][c]) + (sh.part[2][c] + sh.part[3][c])
-                                        : 0.0f;
-                    if (whole) {
-                        sh.fac[c] = v != 0.0f ? 1.0f / v : 0.0f;
-                    } else {
-                        sh.fac[c] = v != 0.0f ? 1.0f : 0.0f;
-                        reinterpret_cast<float2*>(a.ws + a.ml_off)[slot * N + c] = make_float2(-sh.colr[c], v);
+                    for (int i = 0; i < 8; i += 2) {
+                        const float p0 = tree_exp2(x[c + i]), p1 = tree_exp2(x[c + i + 1]);
+                        unpack2(fma2(pack2(p0, p1), inv2, pack2(l[c + i], l[c + i + 1])), &l[c + i], &l[c + i + 1]);
+                        p[i / 2] = h2_as_u32(__floats2half2_rn(p0, p1));
                     }
+                    *reinterpret_cast<uint4*>(prow + ((col0 + c) >> 3) * (16 * kCoreBytes)) = make_uint4(p[0], p[1], p[2], p[3]);
                 }
-                bar_sync(2, ST);
-                const bool odd = sh.odd != 0;
-#pragma unroll 1
-                for (int d = 0; d < S::kDN; ++d) {
-                    const int ch0 = 128 * d + 32 * quad;
-                    if (ch0 >= D) continue;
-                    // lane -> channel: the order of the tile's value rows
-                    const int ch = rows_scheme ? place_channel(ch0 + lane, W, D) : ch0 + lane;
-#pragma unroll 1
-                    for (int c0 = 0; c0 < S::NH; c0 += 8) {
-                        float o[8];
-                        if (w.live) tmem_load(tm_o + d * N + lanes + col0 + c0, o);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int c = col0 + c0 + i, r = row0 + c;
-                            if (r >= a.rows) continue;
-                            const float fc = sh.fac[c];
-                            float v = fc != 0.0f ? o[i] * fc : 0.0f;
-                            if (odd && r < row_end) {   // drafts whose value is not finite, in the rows that see them
-                                const int node = r >> a.gshift;
-                                for (int j = 0; j < w.s.nodes; ++j) {
-                                    const float y = __bfloat162float(a.v[(((int64_t)w.b * a.nodes + j) * H + w.h) * D + ch]);
-                                    if (fabsf(y) < INFINITY) continue;
-                                    if (a.mask ? a.mask[((int64_t)w.b * a.nodes + node) * a.nodes + j] != 0 : j <= node) v += y;
-                                }
-                            }
-                            if (whole)
-                                a.out[(((int64_t)w.b * a.nodes + (r >> a.gshift)) * lo.Hq + w.h * gqa + (r & (gqa - 1))) * D + ch] =
-                                    __float2bfloat16_rn(v);
-                            else
-                                reinterpret_cast<float*>(a.ws + a.o_off)[(slot * N + c) * D + ch] = v;
-                        }
-                    }
-                }
+                smem_to_async();
                 tmem_fence_before();
-                bar_sync(2, ST);
-            } while (w.next(a, N));
-        } else if (warp < S::kSoft + S::kUnpack) {
-            // ======================================================================== unpack
-            const int ut = tid - ST;
-            uint32_t it = 0, staged = 0;
-            // one packed KIVI tile, from wherever its records lie
-            auto kivi_tile = [&](const auto& t, uint64_t* empty) {
-                const bool big = bar_or(1, DT, kivi_bound<DT>(lo, t, 0, ut) >= 32768.0f || kivi_bound<DT>(lo, t, 1, ut) >= 32768.0f);
-                int ke = 0, ve = 0;
-                if (big) {      // outside binary16: the tile's keys or values under a power of two
-                    if (ut < 2) sh.top[ut] = 0u;
-                    bar_sync(1, DT);
-                    for (int kv = 0; kv < 2; ++kv)
-                        atomicMax(&sh.top[kv], __float_as_uint(kivi_bound<DT>(lo, t, kv, ut)));
-                    bar_sync(1, DT);
-                    if (__uint_as_float(sh.top[0]) >= 32768.0f) ke = range_exponent(__uint_as_float(sh.top[0]));
-                    if (__uint_as_float(sh.top[1]) >= 32768.0f) ve = range_exponent(__uint_as_float(sh.top[1]));
-                }
-                if (ut < 128) {
-                    sh.kf[it & 1][ut] = pow2i(ke);
-                    sh.vl[it & 1][ut] = static_cast<float>(ve);
-                }
-                wait(&sh.k_empty, it + 1);
-                if (ke != 0)
-                    kivi_keys_scaled<D, DT>(lo, t, kt, pow2i(-ke), W, ut);
-                else if constexpr (D >= 64) {
-                    if (lo.bits == 2) kivi_keys<D, 2, DT>(a, t, kt, ut);
-                    else if (lo.bits == 4) kivi_keys<D, 4, DT>(a, t, kt, ut);
-                    else kivi_keys<D, 8, DT>(a, t, kt, ut);
-                }
-                if (lo.K > 0) {
-                    bar_sync(1, DT);
-                    kivi_outliers<D, DT>(lo, t, kt, 0, pow2i(-ke), W, ut);
-                }
-                if (rope) {
-                    bar_sync(1, DT);
-                    turn_keys<D, DT>(kt, sh.wt, t.t0, t.cnt, true, ut);
-                }
-                publish(&sh.k_full);
-                wait(&sh.pv_done, it + 1);
-                if (ve != 0)
-                    kivi_values_scaled<D, DT>(lo, t, vt, pow2i(-ve), ut);
-                else if constexpr (D >= 64) {
-                    if (lo.bits == 2) kivi_values<D, 2, DT>(a, t, vt, ut);
-                    else if (lo.bits == 4) kivi_values<D, 4, DT>(a, t, vt, ut);
-                    else kivi_values<D, 8, DT>(a, t, vt, ut);
-                }
-                if (lo.K > 0) {
-                    bar_sync(1, DT);
-                    kivi_outliers<D, DT>(lo, t, vt, 1, pow2i(-ve), W, ut);
-                }
-                publish(&sh.v_full);
-                if (empty && lane == 0) mbar_arrive(empty);
-            };
-            do {
-                for (int tile = w.first; w.live && tile < w.end; ++tile, ++it) {
-                    wait(&sh.s_empty[it & 1], (it >> 1) + 1);       // the factors of two tiles before are read
-                    if (tile >= w.s.packed) {
-                        const int r0 = (tile - w.s.packed) * 128, cnt = w.raw_count(tile), held = w.s.n - w.s.qn - r0;
-                        wait(&sh.k_empty, it + 1);
-                        raw_rows<D, DT>(a, w.b, w.h, w.s, r0, cnt, W, rows_scheme, kt, nullptr, sh.kf[it & 1], sh.vl[it & 1], &sh.odd, 0, ut);
-                        raw_rows<D, DT>(a, w.b, w.h, w.s, r0, cnt, W, rows_scheme, nullptr, nullptr, sh.kf[it & 1], sh.vl[it & 1], &sh.odd, 1, ut);
-                        if (rope) {
-                            bar_sync(1, DT);
-                            turn_keys<D, DT>(kt, sh.wt, (int64_t)w.s.qn + r0, held < cnt ? held : cnt, false, ut);
-                        }
-                        publish(&sh.k_full);
-                        wait(&sh.pv_done, it + 1);
-                        raw_rows<D, DT>(a, w.b, w.h, w.s, r0, cnt, W, rows_scheme, nullptr, vt, sh.kf[it & 1], sh.vl[it & 1], &sh.odd, 1, ut);
-                        publish(&sh.v_full);
-                        continue;
-                    }
-                    const int cnt = w.packed_count(a, tile);
-                    const int64_t t0 = (int64_t)tile * a.TT;
-                    if (a.stages == 0) {
-                        // records too large to pass through shared memory next to the tiles
-                        if (ut < 8 && ut * lo.G < cnt) {
-                            int64_t off = group_offset(lo, a.layer, w.b, w.h, (int64_t)tile * a.TG + ut);
-                            if (off < 0) {
-                                atomicOr(reinterpret_cast<uint32_t*>(a.ws), KVQ_STATUS_BAD_PAGE);
-                                off = lo.data_off + (((int64_t)a.layer * H + w.h) * lo.PG + (tile * a.TG + ut) % lo.PG) * lo.rec;
-                            }
-                            sh.recs[it & 1][ut] = a.cache + off;
-                        }
-                        bar_sync(1, DT);
-                        PackedTile<false> t;
-                        t.recs = sh.recs[it & 1];
-                        t.cnt = cnt;
-                        t.t0 = t0;
-                        kivi_tile(t, nullptr);
-                        continue;
-                    }
-                    const uint32_t sl = a.stages == 2 ? staged & 1 : 0, ph = a.stages == 2 ? staged >> 1 : staged;
-                    ++staged;
-                    const uint8_t* raw = stage + sl * a.stage_bytes;
-                    wait(&sh.stage_full[sl], ph);
-                    if (kivi) {
-                        PackedTile<true> t;
-                        t.base = raw;
-                        t.stride = lo.rec;
-                        t.cnt = cnt;
-                        t.t0 = t0;
-                        kivi_tile(t, &sh.stage_empty[sl]);
-                        continue;
-                    }
-                    if (ut < 128) {
-                        const int tok = fp8 ? packed_token(ut) : ut;
-                        float f = 0.0f, lv = 0.0f;
-                        if (fp8) {
-                            const float* sc = fp8_scale(a, w.h);
-                            f = sc[0];
-                            lv = fast_log2(fabsf(sc[1]));
-                        } else if (tok < cnt) {
-                            const float* sc = reinterpret_cast<const float*>(raw + 256 * row_bytes);
-                            f = sc[tok];
-                            lv = fast_log2(sc[128 + tok]);
-                        }
-                        sh.kf[it & 1][ut] = f;
-                        sh.vl[it & 1][ut] = fmaxf(lv, -110.0f);     // (a scale of 0 belongs to codes of 0)
-                    }
-                    wait(&sh.k_empty, it + 1);
-                    const bool e4m3 = lo.scheme == KVQ_SCHEME_FP8_E4M3, int8 = lo.scheme == KVQ_SCHEME_INT8;
-                    if (fp8) fp8_keys<D, DT>(raw, cnt, e4m3, kt, ut);
-                    else rows_codes<D, DT>(raw, cnt, 0, int8, kt, ut);
-                    publish(&sh.k_full);
-                    wait(&sh.pv_done, it + 1);
-                    const uint8_t* vraw = raw + 128 * row_bytes;
-                    if (fp8) fp8_values<D, DT>(vraw, cnt, e4m3, fp8_scale(a, w.h)[1] < 0.0f, vt, ut);
-                    else rows_codes<D, DT>(vraw, cnt, 1, int8, vt, ut);
-                    publish(&sh.v_full);
-                    if (lane == 0) mbar_arrive(&sh.stage_empty[sl]);
-                }
-            } while (w.next(a, N));
-        } else if (warp == S::kSoft + S::kUnpack) {
-            // ======================================================================= product
-            if (lane == 0) {
-                uint32_t it = 0, seg = 0;
-                const uint64_t dk = mma_desc(smem_addr(kt), D / 8 * kCoreBytes), dq = mma_desc(smem_addr(qt), D / 8 * kCoreBytes);
-                const uint64_t dp = mma_desc(smem_addr(pt), 16 * kCoreBytes);
-                // the scores of tile i
-                auto score = [&](uint32_t i) {
-                    wait(&sh.k_full, i);
-                    wait(&sh.s_empty[i & 1], (i >> 1) + 1);
+                __syncthreads();
+                if (warp == 0 && elect_one()) {
                     tmem_fence_after();
+                    const uint64_t dp = mma_desc(smem_addr(pt), 16 * kCoreBytes);
+                    const int steps = (cnt + 15) >> 4;
+                    const bool mn = !packed || rows_scheme;             // values with channels inside a row
+                    const uint32_t idesc = mn ? mma_idesc(128, N, true, true) : mma_idesc(128, N, false, true);
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k)
-                        mma_f16(tm_s + (i & 1) * N, dk + k * (2 * kCoreBytes >> 4), dq + k * (2 * kCoreBytes >> 4),
-                                mma_idesc(128, N, false, false), k > 0);
-                    mma_commit(&sh.k_empty);
-                    mma_commit(&sh.s_full[i & 1]);
-                    mbar_arrive(&sh.s_full[i & 1]);     // hands the tokens' factors on, too
-                };
-                do {
-                    if (!w.live) continue;
-                    wait(&sh.q_full, seg++);
-                    score(it);
-                    for (int tile = w.first; tile < w.end; ++tile, ++it) {
-                        if (tile + 1 < w.end) score(it + 1);
-                        const bool packed = tile < w.s.packed, mn = !packed || rows_scheme;
-                        const int steps = ((packed ? w.packed_count(a, tile) : w.raw_count(tile)) + 15) >> 4;
-                        wait(&sh.v_full, it);
-                        wait(&sh.p_full, it);
-                        tmem_fence_after();
+                    for (int d = 0; d < S::kDN; ++d) {
+                        const uint64_t dv = mma_desc(smem_addr(vt) + d * 32768, 16 * kCoreBytes);
 #pragma unroll
-                        for (int d = 0; d < S::kDN; ++d) {
-                            const uint64_t dv = mma_desc(smem_addr(vt) + d * 32768, 16 * kCoreBytes);
-                            for (int k = 0; k < steps; ++k)
-                                mma_f16(tm_o + d * N, dv + k * (2 * kCoreBytes >> 4), dp + k * (2 * kCoreBytes >> 4),
-                                        mma_idesc(128, N, mn, true), tile > w.first || k > 0);
-                        }
-                        mma_commit(&sh.pv_done);
+                        for (int k = 0; k < 8; ++k)
+                            if (k < steps)
+                                mma_f16(tm_o + d * N, dv + k * (2 * kCoreBytes >> 4), dp + k * (2 * kCoreBytes >> 4), idesc,
+                                        tile > first || k > 0);
                     }
-                } while (w.next(a, N));
-                mma_commit(&sh.done);
-                if (!mbar_wait_clock(&sh.done, 0)) atomicOr(reinterpret_cast<uint32_t*>(a.ws), KVQ_STATUS_TIMEOUT);
-            }
-        } else if (lane == 0 && a.stages > 0) {
-            // ========================================================================== copy
-            uint32_t staged = 0;
-            do {
-                for (int tile = w.first; w.live && tile < w.end && tile < w.s.packed; ++tile) {
-                    const uint32_t sl = a.stages == 2 ? staged & 1 : 0, ph = a.stages == 2 ? staged >> 1 : staged;
-                    wait(&sh.stage_empty[sl], ph + 1);
-                    if (dead()) break;
-                    ++staged;
-                    uint8_t* to = stage + sl * a.stage_bytes;
-                    uint64_t* bar = &sh.stage_full[sl];
-                    const int cnt = w.packed_count(a, tile);
-                    const int64_t t0 = (int64_t)tile * a.TT;
-                    if (kivi) {
-                        const int g0 = tile * a.TG, all = w.s.qn / lo.G - g0, ng = all < a.TG ? all : a.TG;
-                        mbar_arrive_expect_tx(bar, static_cast<uint32_t>(ng * lo.rec));
-                        if (lo.PG == 0) {
-                            bulk_copy_g2s(to, a.cache + group_offset(lo, a.layer, w.b, w.h, g0), ng * lo.rec, bar);
-                        } else {
-                            for (int g = 0; g < ng; ++g) {
-                                int64_t off = group_offset(lo, a.layer, w.b, w.h, g0 + g);
-                                if (off < 0) {  // a table entry outside the pool: page 0 in its place, reported
-                                    atomicOr(reinterpret_cast<uint32_t*>(a.ws), KVQ_STATUS_BAD_PAGE);
-                                    off = lo.data_off + (((int64_t)a.layer * H + w.h) * lo.PG + (g0 + g) % lo.PG) * lo.rec;
-                                }
-                                bulk_copy_g2s(to + g * lo.rec, a.cache + off, lo.rec, bar);
-                            }
-                        }
-                    } else {
-                        const int c16 = (cnt + 15) & ~15;
-                        const uint8_t* base = a.cache + lo.data_off + unit_index(lo, a.layer, w.b, w.h) * lo.unit;
-                        const uint32_t bytes = static_cast<uint32_t>(c16 * row_bytes);
-                        mbar_arrive_expect_tx(bar, 2 * bytes + (rows_scheme ? 8 * c16 : 0));
-                        bulk_copy_g2s(to, base + t0 * row_bytes, bytes, bar);
-                        bulk_copy_g2s(to + 128 * row_bytes, base + (lo.T16 + t0) * row_bytes, bytes, bar);
-                        if (rows_scheme) {
-                            const uint8_t* sc = base + 2 * (int64_t)lo.T16 * row_bytes;
-                            bulk_copy_g2s(to + 256 * row_bytes, sc + 4 * t0, 4 * c16, bar);
-                            bulk_copy_g2s(to + 256 * row_bytes + 512, sc + 4 * (lo.T16 + t0), 4 * c16, bar);
-                        }
-                    }
+                    mma_commit(&sh.pv_done);
                 }
-            } while (w.next(a, N));
-            // where a wait gave up, the copies in flight land before the block ends
-            if (dead())
-                for (uint32_t i = staged > static_cast<uint32_t>(a.stages) ? staged - a.stages : 0; i < staged; ++i)
-                    mbar_wait_clock(&sh.stage_full[a.stages == 2 ? i & 1 : 0], (a.stages == 2 ? i >> 1 : i) & 1);
-        }
+                __syncwarp();
+            }
+            // ---------------------------------------------------------- the segment's result
+            if (live) wait(&sh.pv_done, it + 1);
+            tmem_fence_after();
+            // the sums over a column's tokens
+#pragma unroll
+            for (int i = 0; i < NH; ++i) {
+                float v = l[i];
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+                if (lane == 0) sh.part[quad][col0 + i] = v;
+            }
+            __syncthreads();
+            finish_segment<N, D, rows_scheme>(a, first, tm_o + lanes + col0, row0, row_end, W, sh);
+            tmem_fence_before();
+            __syncthreads();
+            tmem_fence_after();
+            if (tid == 0) sh.more = w.next(a, N);
+            __syncthreads();
+        } while (sh.more);
+        // where a wait gave up, the copies in flight land before the block ends
+        if (staged_tiles && tid == 0 && sh.dead)
+            for (uint32_t i = used; i < used + a.stages; ++i) mbar_wait_asleep(&sh.stage_full[slot_of(i)], turn_of(i) & 1);
     }
     __syncthreads();
     if (warp == 0) tmem_free(tm_s, S::kCols);
@@ -1403,10 +1471,5 @@ __global__ void __launch_bounds__(kMergeThreads) k_tree_merge(const __grid_const
             __float2bfloat16_rn(L != 0.0f ? O / L : 0.0f);
     }
 }
-
-int launch_tree_d32(TreeArgs& a, int N, cudaStream_t stream);
-int launch_tree_d64(TreeArgs& a, int N, cudaStream_t stream);
-int launch_tree_d128(TreeArgs& a, int N, cudaStream_t stream);
-int launch_tree_d256(TreeArgs& a, int N, cudaStream_t stream);
 
 }  // namespace kvq

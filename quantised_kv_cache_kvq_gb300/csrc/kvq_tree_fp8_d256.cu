@@ -1,0 +1,6 @@
+// kvq_tree_fp8_d256.cu -- tree attention: FP8, 256 channels (kernel: kvq_tree.cuh).
+#include "kvq_tree_launch.cuh"
+
+namespace kvq {
+int launch_tree_fp8_d256(TreeArgs& a, int N, cudaStream_t stream) { return launch_tree_kind<256, kFp8>(a, N, stream); }
+}  // namespace kvq

@@ -1,0 +1,6 @@
+// kvq_tree_kivi4_d64.cu -- tree attention: 4-bit KIVI, 64 channels (kernel: kvq_tree.cuh).
+#include "kvq_tree_launch.cuh"
+
+namespace kvq {
+int launch_tree_kivi4_d64(TreeArgs& a, int N, cudaStream_t stream) { return launch_tree_kind<64, kKivi4>(a, N, stream); }
+}  // namespace kvq

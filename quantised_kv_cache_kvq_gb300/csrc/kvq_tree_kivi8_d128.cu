@@ -1,0 +1,6 @@
+// kvq_tree_kivi8_d128.cu -- tree attention: 8-bit KIVI, 128 channels (kernel: kvq_tree.cuh).
+#include "kvq_tree_launch.cuh"
+
+namespace kvq {
+int launch_tree_kivi8_d128(TreeArgs& a, int N, cudaStream_t stream) { return launch_tree_kind<128, kKivi8>(a, N, stream); }
+}  // namespace kvq
