@@ -537,88 +537,105 @@ __device__ __forceinline__ const float* fp8_scale(const TreeArgs& a, int h) {
     return reinterpret_cast<const float*>(a.cache + a.lo.scales_off) + ((int64_t)a.layer * a.lo.H + h) * 2;
 }
 
-// 16 bf16 channels as binary16 pairs times 2^-e.  zero: what is not finite becomes 0.
-__device__ __forceinline__ void half_words(const uint32_t (&w)[8], float f, bool zero, uint32_t (&o)[8]) {
+// 16 bf16 channels as binary16 pairs times f.
+__device__ __forceinline__ void half_words(const uint32_t (&w)[8], float f, uint32_t (&o)[8]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        float x = __uint_as_float(w[i] << 16), y = __uint_as_float(w[i] & 0xffff0000u);
-        if (zero) {
-            x = fabsf(x) < INFINITY ? x : 0.0f;
-            y = fabsf(y) < INFINITY ? y : 0.0f;
-        }
-        o[i] = h2_as_u32(__floats2half2_rn(x * f, y * f));
-    }
+    for (int i = 0; i < 8; ++i)
+        o[i] = h2_as_u32(__floats2half2_rn(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xffff0000u) * f));
 }
-// Largest finite |x| of 16 bf16 channels; *bad: one is not finite.
-__device__ __forceinline__ float unit_top(const uint32_t (&w)[8], bool* bad) {
-    float top = 0.0f;
+// Largest magnitude of 16 bf16 channels, as a pattern (0x7f80 and above: not finite).
+__device__ __forceinline__ uint32_t unit_top(const uint32_t (&w)[8]) {
+    uint32_t m = w[0] & 0x7fff7fffu;
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+    return max(m & 0xffffu, m >> 16);
+}
+// The same over the finite ones, which are left alone where `keep`; the others become 0 if not.
+__device__ __forceinline__ uint32_t finite_top(uint32_t (&w)[8], bool keep) {
+    uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float x = fabsf(__uint_as_float(w[i] << 16)), y = fabsf(__uint_as_float(w[i] & 0xffff0000u));
-        *bad |= !(x < INFINITY) || !(y < INFINITY);
-        top = fmaxf(top, fmaxf(x < INFINITY ? x : 0.0f, y < INFINITY ? y : 0.0f));
+        const uint32_t lo = w[i] & 0x7fffu, hi = (w[i] >> 16) & 0x7fffu;
+        if (lo < 0x7f80u) m = max(m, lo);
+        else if (!keep) w[i] &= 0xffff0000u;
+        if (hi < 0x7f80u) m = max(m, hi);
+        else if (!keep) w[i] &= 0x0000ffffu;
     }
-    return top;
+    return m;
+}
+// Largest finite magnitude of the row that lanes l, l + 8, l + 16 and l + 24 hold.
+template <int STEPS>
+__device__ __forceinline__ float row_top(uint32_t (&w)[STEPS][8], bool keep, bool* odd) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) m = max(m, unit_top(w[i]));
+    if (m >= 0x7f80u) {
+        *odd = true;
+        m = 0;
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) m = max(m, finite_top(w[i], keep));
+    }
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 8));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 16));
+    return __uint_as_float(m << 16);
 }
 __device__ __forceinline__ void load_words(const uint16_t* p, uint32_t (&w)[8]) {
     const uint4 a = reinterpret_cast<const uint4*>(p)[0], b = reinterpret_cast<const uint4*>(p)[1];
     w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w; w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
 }
 
-// bf16 rows (the window's tokens, then the drafts) [r0, r0 + cnt) of unit (b, h): the keys
-// (kv = 0) or values into their tile (none: NULL) and their powers of two.  A warp takes an
-// octet of rows, a lane 16 channels of one row at a time; each row is scaled by its own largest
-// element.  *bad: a draft's value is not finite (it is 0 in the tile).
+// bf16 rows (the window's tokens, then the drafts) [r0, r0 + cnt) of unit (b, h): keys and
+// values into their tiles, with their powers of two.  A warp takes an octet of rows, a lane 16
+// channels of one row at a time; each row is scaled by its own largest element.  *bad: a
+// draft's value is not finite (it is 0 in the tile).
 template <int D, int DT>
-__device__ __noinline__ void raw_rows(const TreeArgs& a, int b, int h, const TreeSeq s, int r0, int cnt, int W,
-                                         bool paired_values, uint8_t* kt, uint8_t* vt, float* kf, float* vlog,
-                                         int* bad, int kv, int tid) {
+__device__ __noinline__ void raw_rows(const TreeArgs& a, int b, int h, int n, int qn, int r0, int cnt, int W, bool paired_values,
+                                      uint8_t* kt, uint8_t* vt, float* kf, float* vlog, int* bad, int tid) {
     constexpr int UNITS = D / 16, STEPS = (UNITS + 3) / 4;
-    const int warp = tid >> 5, lane = tid & 31;
-    const int window = s.n - s.qn;
-    const uint32_t slot0 = static_cast<uint32_t>(s.qn) % static_cast<uint32_t>(a.lo.C > 0 ? a.lo.C : 1);
+    const int warp = tid >> 5, lane = tid & 31, window = n - qn, C = a.lo.C;
+    const uint32_t slot0 = C > 0 ? static_cast<uint32_t>(qn) % static_cast<uint32_t>(C) : 0u;
+    const uint16_t* ring = reinterpret_cast<const uint16_t*>(a.cache + a.lo.ring_off) + unit_index(a.lo, a.layer, b, h) * C * (2 * D);
+    const int64_t draft0 = (((int64_t)b * a.nodes - window) * a.lo.H + h) * D;      // row r: + r H D
     for (int o = warp; o < 16; o += DT / 32) {
         const int row = 8 * o + (lane & 7), r = r0 + row;
         if ((8 * o & ~15) >= cnt) break;
+        uint32_t w[2][STEPS][8];
         const uint16_t *kp = nullptr, *vp = nullptr;
         if (row < cnt) {
             if (r < window) {
                 uint32_t slot = slot0 + r;                  // window token r is in slot (qn + r) mod C
-                if (slot >= static_cast<uint32_t>(a.lo.C)) slot -= a.lo.C;
-                kp = reinterpret_cast<const uint16_t*>(a.cache + a.lo.ring_off +
-                                                       (unit_index(a.lo, a.layer, b, h) * a.lo.C + slot) * (4 * D));
+                if (slot >= static_cast<uint32_t>(C)) slot -= C;
+                kp = ring + (int64_t)slot * (2 * D);
                 vp = kp + D;
             } else {
-                const int64_t at = (((int64_t)b * a.nodes + (r - window)) * a.lo.H + h) * D;
+                const int64_t at = draft0 + (int64_t)r * a.lo.H * D;
                 kp = reinterpret_cast<const uint16_t*>(a.k) + at;
                 vp = reinterpret_cast<const uint16_t*>(a.v) + at;
             }
         }
-        {
-            const uint16_t* p = kv ? vp : kp;
-            uint32_t w[STEPS][8];
-            float top = 0.0f;
-            bool odd = false;
 #pragma unroll
-            for (int i = 0; i < STEPS; ++i) {
-                const int unit = (lane >> 3) + 4 * i;
+        for (int i = 0; i < STEPS; ++i) {
+            const int unit = (lane >> 3) + 4 * i;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) w[i][j] = 0u;
-                if (p && unit < UNITS) load_words(p + 16 * unit, w[i]);
-                top = fmaxf(top, unit_top(w[i], &odd));
+            for (int j = 0; j < 8; ++j) w[0][i][j] = w[1][i][j] = 0u;
+            if (kp && unit < UNITS) {
+                load_words(kp + 16 * unit, w[0][i]);
+                load_words(vp + 16 * unit, w[1][i]);
             }
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-            const int e = range_exponent(top);
-            const float f = pow2i(-e);
-            const bool draft = r >= window;
+        }
+        const bool draft = r >= window;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+            bool odd = false;
+            const int e = range_exponent(row_top(w[kv], kv == 0 || !draft, &odd));
             if (kv && odd && draft) *bad = 1;
+            const float f = pow2i(-e);
 #pragma unroll
             for (int i = 0; i < STEPS; ++i) {
                 const int unit = (lane >> 3) + 4 * i;
-                if (unit >= UNITS || !(kv ? vt : kt)) continue;
+                if (unit >= UNITS) continue;
                 uint32_t hw[8];
-                half_words(w[i], f, kv && draft, hw);
+                half_words(w[kv][i], f, hw);
                 if (kv == 0) {
                     store_unit<D>(kt, row, unit, hw, W);
                 } else {
@@ -629,11 +646,9 @@ __device__ __noinline__ void raw_rows(const TreeArgs& a, int b, int h, const Tre
                     *reinterpret_cast<uint4*>(at + 16 * kCoreBytes) = make_uint4(pw[4], pw[5], pw[6], pw[7]);
                 }
             }
-            if (lane < 8 && kf) {
-                if (kv)
-                    vlog[row] = static_cast<float>(e);
-                else
-                    kf[row] = pow2i(e);
+            if (lane < 8) {
+                if (kv) vlog[row] = static_cast<float>(e);
+                else kf[row] = pow2i(e);
             }
         }
     }
@@ -739,6 +754,11 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
+// Where block j of nb's share of `total` tiles begins: total j / nb (in 32 bits where they do).
+__device__ __forceinline__ int64_t share_start(int64_t total, int64_t j, int64_t nb) {
+    if (total < (1 << 21)) return static_cast<uint32_t>(total) * static_cast<uint32_t>(j) / static_cast<uint32_t>(nb);
+    return total * j / nb;
+}
 // A block's walk over its share of the tiles: segments, each the tiles [first, end) of one row
 // tile of one KV head.
 struct TreeWalk {
@@ -755,8 +775,9 @@ struct TreeWalk {
         b = b_;
         left = n;
         s = tree_seq(a, b, N);
-        const int64_t per = tree_head_tiles(a, s), in = at % per, run = (int64_t)s.live * s.tiles;
-        h = static_cast<int>(at / per);
+        const int64_t per = tree_head_tiles(a, s), run = (int64_t)s.live * s.tiles;
+        h = static_cast<int>(at >> 31 ? at / per : static_cast<uint32_t>(at) / static_cast<uint32_t>(per));
+        const int in = static_cast<int>(at - h * per);
         rt = static_cast<int>(in < run ? in / s.tiles : s.live + (in - run));
         first = static_cast<int>(in < run ? in % s.tiles : 0);
         segment();
@@ -798,7 +819,7 @@ struct TreeShared {
     float fac[N], part[4][N];       // per column: factors; per quadrant: maxima, sums
     float kf[128], vl[128];         // a raw row's score factor and log2 of its value scale
     float wt[D / 2];                // rotary frequencies in the order of the key tile
-    int64_t scan[32], start[2];
+    int64_t scan[32], start[3];
     uint64_t stage_full[2], s_full, pv_done;
     const uint8_t* recs[8];         // records read in place
     int qtop, qlow;                 // exponents of the largest and the smallest query
@@ -845,28 +866,23 @@ __device__ __noinline__ float2 load_queries(const TreeArgs& a, int row0, int row
         sh.qlow = 200;
     }
     __syncthreads();
-    auto query = [&](int o, uint32_t (&q)[STEPS][8]) {
-        const int r = row0 + 8 * o + (lane & 7);
-        const uint16_t* p = nullptr;
-        if (r < row_end)
-            p = reinterpret_cast<const uint16_t*>(a.q) +
-                (((int64_t)w.b * a.nodes + (r >> a.gshift)) * a.lo.Hq + w.h * gqa + (r & (gqa - 1))) * D;
-        float mx = 0.0f;
-        bool odd = false;
+    // (at most one octet per warp: 16 columns have 2, 64 have 8 of 8 warps, 128 have 16 of 16)
+    static_assert(N / 8 <= WARPS, "");
+    uint32_t q[STEPS][8];
+    const int c = 8 * warp + (lane & 7), r = row0 + c;
+    float mx = 0.0f;
+    if (warp < N / 8) {
+        const uint16_t* p = reinterpret_cast<const uint16_t*>(a.q) +
+                            (((int64_t)w.b * a.nodes + (r >> a.gshift)) * a.lo.Hq + w.h * gqa + (r & (gqa - 1))) * D;
 #pragma unroll
         for (int i = 0; i < STEPS; ++i) {
             const int unit = (lane >> 3) + 4 * i;
 #pragma unroll
             for (int j = 0; j < 8; ++j) q[i][j] = 0u;
-            if (p && unit < UNITS) load_words(p + 16 * unit, q[i]);
-            mx = fmaxf(mx, unit_top(q[i], &odd));
+            if (r < row_end && unit < UNITS) load_words(p + 16 * unit, q[i]);
         }
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-        return fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-    };
-    for (int o = warp; o < N / 8; o += WARPS) {
-        uint32_t q[STEPS][8];
-        const float mx = query(o, q);
+        bool odd = false;
+        mx = row_top(q, true, &odd);
         if (lane < 8 && mx > 0.0f) {
             atomicMax(&sh.qtop, range_exponent(mx));
             atomicMin(&sh.qlow, range_exponent(mx));
@@ -875,17 +891,15 @@ __device__ __noinline__ float2 load_queries(const TreeArgs& a, int row0, int row
     __syncthreads();
     const bool mixed = sh.qtop - sh.qlow > 20;
     const int common = sh.qtop > -200 ? sh.qtop : 0;
-    for (int o = warp; o < N / 8; o += WARPS) {
-        uint32_t q[STEPS][8];
-        const float mx = query(o, q);
-        const int c = 8 * o + (lane & 7), e = mixed ? range_exponent(mx) : common;
+    if (warp < N / 8) {
+        const int e = mixed ? range_exponent(mx) : common;
         const float f = pow2i(-e);
 #pragma unroll
         for (int i = 0; i < STEPS; ++i) {
             const int unit = (lane >> 3) + 4 * i;
             if (unit >= UNITS) continue;
             uint32_t hw[8];
-            half_words(q[i], f, false, hw);
+            half_words(q[i], f, hw);
             store_unit<D>(qt, c, unit, hw, W);
         }
         if (lane < 8) {
@@ -921,6 +935,9 @@ __device__ __noinline__ void finish_segment(const TreeArgs& a, int first, uint32
     }
     __syncthreads();
     const bool odd = sh.odd != 0;
+    const int gmask = lo.gqa - 1, out_row = lo.Hq * D;
+    __nv_bfloat16* out = a.out + ((int64_t)w.b * a.nodes * lo.Hq + w.h * lo.gqa) * D;
+    float* part = reinterpret_cast<float*>(a.ws + a.o_off) + slot * N * D;
 #pragma unroll 1
     for (int d = 0; d < S::kDN; ++d) {
         const int ch0 = 128 * d + 32 * quad;
@@ -928,28 +945,39 @@ __device__ __noinline__ void finish_segment(const TreeArgs& a, int first, uint32
         // lane -> channel: the order of the tile's value rows
         const int ch = ROWS ? place_channel(ch0 + lane, W, D) : ch0 + lane;
 #pragma unroll 1
-        for (int c0 = 0; c0 < S::NH; c0 += 8) {
-            float o[8];
-            if (w.live) tmem_load(tm + d * N + c0, o);
+        for (int c0 = 0; c0 < S::NH; c0 += S::NH < 16 ? 8 : 16) {
+            constexpr int Q = S::NH < 16 ? 8 : 16;
+            float o[Q];
+            if (w.live) {
+                tmem_load(tm + d * N + c0, o);
+            } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int c = col0 + c0 + i, r = row0 + c;
-                if (r >= a.rows) continue;
-                const float fc = sh.fac[c];
-                float v = fc != 0.0f ? o[i] * fc : 0.0f;
-                if (odd && r < row_end) {   // drafts whose value is not finite, in the rows that see them
-                    const int node = r >> a.gshift;
-                    for (int j = 0; j < w.s.nodes; ++j) {
-                        const float y = __bfloat162float(a.v[(((int64_t)w.b * a.nodes + j) * lo.H + w.h) * D + ch]);
-                        if (fabsf(y) < INFINITY) continue;
-                        if (a.mask ? a.mask[((int64_t)w.b * a.nodes + node) * a.nodes + j] != 0 : j <= node) v += y;
+                for (int i = 0; i < Q; ++i) o[i] = 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < Q; ++i) {
+                const float fc = sh.fac[col0 + c0 + i];
+                o[i] = fc != 0.0f ? o[i] * fc : 0.0f;
+            }
+            if (odd) {      // drafts whose value is not finite, in the rows that see them
+                for (int j = 0; j < w.s.nodes; ++j) {
+                    const float y = __bfloat162float(a.v[(((int64_t)w.b * a.nodes + j) * lo.H + w.h) * D + ch]);
+                    if (fabsf(y) < INFINITY) continue;
+#pragma unroll
+                    for (int i = 0; i < Q; ++i) {
+                        const int r = row0 + col0 + c0 + i, node = r >> a.gshift;
+                        if (r < row_end && (a.mask ? a.mask[((int64_t)w.b * a.nodes + node) * a.nodes + j] != 0 : j <= node)) o[i] += y;
                     }
                 }
+            }
+#pragma unroll
+            for (int i = 0; i < Q; ++i) {
+                const int c = col0 + c0 + i, r = row0 + c;
+                if (r >= a.rows) break;
                 if (whole)
-                    a.out[(((int64_t)w.b * a.nodes + (r >> a.gshift)) * lo.Hq + w.h * lo.gqa + (r & (lo.gqa - 1))) * D + ch] =
-                        __float2bfloat16_rn(v);
+                    out[(r >> a.gshift) * out_row + (r & gmask) * D + ch] = __float2bfloat16_rn(o[i]);
                 else
-                    reinterpret_cast<float*>(a.ws + a.o_off)[(slot * N + c) * D + ch] = v;
+                    part[c * D + ch] = o[i];
             }
         }
     }
@@ -1094,22 +1122,24 @@ __global__ void __launch_bounds__(TreeShape<N, D>::kThreads, TreeShape<N, D>::kB
     grid_launch_dependents();
     // this block's tiles: positions [x0, x1) of all tiles, in the order sequence, KV head, row
     // tile, tile
-    const int64_t total = tree_total<NT>(a, N, sh.scan);
+    int64_t total, mine = tid < lo.B ? H * tree_head_tiles(a, tree_seq(a, tid, N)) : 0;
+    int64_t at = block_scan<NT>(mine, sh.scan, &total);
+    if (lo.B > NT) total = tree_total<NT>(a, N, sh.scan);
     const int64_t nb = total < a.NB ? total : a.NB;     // blocks with a share
-    const int64_t x0 = total * blockIdx.x / nb, x1 = total * (blockIdx.x + 1) / nb;
-    {
-        int64_t base = 0;
-        for (int b0 = 0; b0 < lo.B; b0 += NT) {
-            const int b = b0 + tid;
-            const int64_t w = b < lo.B ? H * tree_head_tiles(a, tree_seq(a, b, N)) : 0;
-            int64_t sum;
-            const int64_t at = base + block_scan<NT>(w, sh.scan, &sum);
-            if (at <= x0 && x0 < at + w) {
-                sh.start[0] = b;
-                sh.start[1] = x0 - at;
-            }
-            base += sum;
+    const int64_t x0 = share_start(total, blockIdx.x, nb), x1 = share_start(total, blockIdx.x + 1, nb);
+    for (int b0 = 0;;) {
+        if (at <= x0 && x0 < at + mine) {
+            sh.start[0] = b0 + tid;
+            sh.start[1] = x0 - at;
         }
+        if ((b0 += NT) >= lo.B) break;
+        const int64_t base = at + mine;                 // of the last thread: the next round's start
+        if (tid == NT - 1) sh.start[2] = base;
+        __syncthreads();
+        const int b = b0 + tid;
+        int64_t sum;
+        mine = b < lo.B ? H * tree_head_tiles(a, tree_seq(a, b, N)) : 0;
+        at = sh.start[2] + block_scan<NT>(mine, sh.scan, &sum);
     }
     tmem_fence_before();
     __syncthreads();
@@ -1117,6 +1147,7 @@ __global__ void __launch_bounds__(TreeShape<N, D>::kThreads, TreeShape<N, D>::kB
     const uint32_t tm_s = sh.tmem, tm_o = tm_s + N, my_s = tm_s + lanes + col0;
 
     auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (mbar_try_wait(bar, parity & 1)) return;
         if (*static_cast<volatile int*>(&sh.dead)) return;
         if (!mbar_wait_asleep(bar, parity & 1)) {
             sh.dead = 1;
@@ -1169,8 +1200,7 @@ __global__ void __launch_bounds__(TreeShape<N, D>::kThreads, TreeShape<N, D>::kB
                 if (!packed) {
                     const int r0 = (tile - w.s.packed) * 128, held = w.s.n - w.s.qn - r0;
                     wait(&sh.pv_done, it + 1);                          // the rows write both tiles
-                    raw_rows<D, CT>(a, w.b, w.h, w.s, r0, cnt, W, rows_scheme, kt, nullptr, sh.kf, sh.vl, &sh.odd, 0, tid);
-                    raw_rows<D, CT>(a, w.b, w.h, w.s, r0, cnt, W, rows_scheme, nullptr, vt, sh.kf, sh.vl, &sh.odd, 1, tid);
+                    raw_rows<D, CT>(a, w.b, w.h, w.s.n, w.s.qn, r0, cnt, W, rows_scheme, kt, vt, sh.kf, sh.vl, &sh.odd, tid);
                     if (rope) {
                         __syncthreads();
                         turn_keys<D, CT>(kt, sh.wt, (int64_t)w.s.qn + r0, held < cnt ? held : cnt, false, tid);
@@ -1273,6 +1303,7 @@ __global__ void __launch_bounds__(TreeShape<N, D>::kThreads, TreeShape<N, D>::kB
                 // ---- softmax
                 const float inv = tree_exp2(-lv);
                 const uint64_t f2 = pack2(f, f), lv2 = pack2(lv, lv), inv2 = pack2(inv, inv);
+                const uint8_t* mask = a.mask ? a.mask + (int64_t)w.b * a.nodes * a.nodes : nullptr;
                 // x + log2 s of B columns from c0 on, less the references if REF
                 auto scores = [&](int c0, float (&x)[B], bool ref) {
                     tmem_load(my_s + c0, x);
@@ -1297,8 +1328,7 @@ __global__ void __launch_bounds__(TreeShape<N, D>::kThreads, TreeShape<N, D>::kB
                             bool see = valid;
                             if (draft >= 0) {
                                 const int r = row0 + col0 + c0 + i, node = r >> a.gshift;
-                                see = r < row_end && (a.mask ? a.mask[((int64_t)w.b * a.nodes + node) * a.nodes + draft] != 0
-                                                             : draft <= node);
+                                see = r < row_end && (mask ? mask[node * a.nodes + draft] != 0 : draft <= node);
                             }
                             x[i] = see ? x[i] : -INFINITY;
                         }
@@ -1372,11 +1402,16 @@ __global__ void __launch_bounds__(TreeShape<N, D>::kThreads, TreeShape<N, D>::kB
 #pragma unroll
                     for (int d = 0; d < S::kDN; ++d) {
                         const uint64_t dv = mma_desc(smem_addr(vt) + d * 32768, 16 * kCoreBytes);
+                        if (steps == 8) {
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            if (k < steps)
+                            for (int k = 0; k < 8; ++k)
                                 mma_f16(tm_o + d * N, dv + k * (2 * kCoreBytes >> 4), dp + k * (2 * kCoreBytes >> 4), idesc,
                                         tile > first || k > 0);
+                        } else {
+                            for (int k = 0; k < steps; ++k)
+                                mma_f16(tm_o + d * N, dv + k * (2 * kCoreBytes >> 4), dp + k * (2 * kCoreBytes >> 4), idesc,
+                                        tile > first || k > 0);
+                        }
                     }
                     mma_commit(&sh.pv_done);
                 }
@@ -1385,13 +1420,16 @@ __global__ void __launch_bounds__(TreeShape<N, D>::kThreads, TreeShape<N, D>::kB
             // ---------------------------------------------------------- the segment's result
             if (live) wait(&sh.pv_done, it + 1);
             tmem_fence_after();
-            // the sums over a column's tokens
+            // the sums over a column's tokens, through the key tile's memory: [column][token]
+            float* sums = reinterpret_cast<float*>(smem);
 #pragma unroll
-            for (int i = 0; i < NH; ++i) {
-                float v = l[i];
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-                if (lane == 0) sh.part[quad][col0 + i] = v;
+            for (int i = 0; i < NH; ++i) sums[(col0 + i) * 128 + row] = l[i];
+            __syncthreads();
+            for (int i = tid; i < 4 * N; i += CT) {         // a quarter of a column each, in a fixed order
+                float v = 0.0f;
+#pragma unroll 8
+                for (int j = 0; j < 32; ++j) v += sums[32 * i + ((j + lane) & 31)];
+                sh.part[i & 3][i >> 2] = v;
             }
             __syncthreads();
             finish_segment<N, D, rows_scheme>(a, first, tm_o + lanes + col0, row0, row_end, W, sh);
@@ -1439,9 +1477,9 @@ __global__ void __launch_bounds__(kMergeThreads) k_tree_merge(const __grid_const
     const int64_t y0 = start + h * tree_head_tiles(a, s) + (int64_t)rt * s.tiles, y1 = y0 + s.tiles;
     // block j has the positions [total j / nb, total (j + 1) / nb)
     int64_t j0 = y0 * nb / total, j1;
-    while (total * (j0 + 1) / nb <= y0) ++j0;
-    while (total * j0 / nb > y0) --j0;
-    for (j1 = j0; total * (j1 + 1) / nb < y1;) ++j1;
+    while (share_start(total, j0 + 1, nb) <= y0) ++j0;
+    while (share_start(total, j0, nb) > y0) --j0;
+    for (j1 = j0; share_start(total, j1 + 1, nb) < y1;) ++j1;
     // every block waits, also one with nothing to join: the launch after this one may rely on it
     grid_dependency_wait();
     if (rt >= s.live || j0 == j1) return;
