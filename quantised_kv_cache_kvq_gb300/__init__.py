@@ -53,17 +53,36 @@ def max_pages(cfg) -> int:
     return (ng + cfg.page_groups - 1) // cfg.page_groups if cfg.page_groups > 0 else 0
 
 
+def _fits(x, shape, dtype, device):
+    """Whether the library reads tensor x rightly: a contiguous tensor of this shape and type on
+    this device, or in page-locked host memory."""
+    return (x.shape == shape and x.dtype == dtype and x.is_contiguous()
+            and (x.device == device or not x.is_cuda and (x.numel() == 0 or x.is_pinned())))
+
+
 def _expect(name, x, shape, dtype, device):
     """Refuses a tensor that the library would read wrongly."""
-    kinds = dtype if isinstance(dtype, tuple) else (dtype,)
-    if tuple(x.shape) != tuple(shape) or x.dtype not in kinds or not x.is_contiguous():
-        raise ValueError("%s: expected a contiguous %s tensor of shape %s, got %s %s%s" % (
-            name, " or ".join(str(k) for k in kinds), tuple(shape), x.dtype, tuple(x.shape),
-            "" if x.is_contiguous() else " (not contiguous)"))
-    if x.is_cuda and x.device != device:
-        raise ValueError("%s is on %s, not on %s" % (name, x.device, device))
-    if not x.is_cuda and x.numel() and not x.is_pinned():
-        raise ValueError("%s: host memory must be page-locked" % name)
+    if not _fits(x, shape, dtype, device):
+        raise ValueError("%s: expected a contiguous %s tensor of shape %s on %s (or page-locked), got %s %s on %s%s" % (
+            name, dtype, tuple(shape), device, x.dtype, tuple(x.shape), x.device,
+            "" if x.is_contiguous() else ", not contiguous"))
+
+
+class _on:
+    """torch.cuda.device, where the device is not the current one already."""
+
+    def __init__(self, device):
+        self.device, self.guard = device, None
+
+    def __enter__(self):
+        import torch
+        if torch.cuda.current_device() != self.device.index:
+            self.guard = torch.cuda.device(self.device)
+            self.guard.__enter__()
+
+    def __exit__(self, *e):
+        if self.guard is not None:
+            self.guard.__exit__(*e)
 
 
 class QuantizedKVCache:
@@ -118,28 +137,28 @@ class QuantizedKVCache:
         workspace: tree_workspace(nodes), by default one that the cache keeps for each number
         of nodes."""
         import torch
-        c = self.cfg
+        c, device, bf16 = self.cfg, self.device, torch.bfloat16
+        batch, heads, D = c.batch, c.kv_heads, c.head_dim
         nodes = q.shape[1] if q.dim() == 4 else 0
-        bf16 = torch.bfloat16
-        _expect("q", q, (c.batch, nodes, c.q_heads, c.head_dim), bf16, self.device)
-        _expect("k_draft", k_draft, (c.batch, nodes, c.kv_heads, c.head_dim), bf16, self.device)
-        _expect("v_draft", v_draft, (c.batch, nodes, c.kv_heads, c.head_dim), bf16, self.device)
+        _expect("q", q, (batch, nodes, c.q_heads, D), bf16, device)
+        _expect("k_draft", k_draft, (batch, nodes, heads, D), bf16, device)
+        _expect("v_draft", v_draft, (batch, nodes, heads, D), bf16, device)
         if mask is not None:
-            _expect("mask", mask, (c.batch, nodes, nodes), (torch.bool, torch.uint8), self.device)
+            _expect("mask", mask, (batch, nodes, nodes), torch.uint8 if mask.dtype == torch.uint8 else torch.bool, device)
         if n_nodes is not None:
-            _expect("n_nodes", n_nodes, (c.batch,), torch.int32, self.device)
-        with torch.cuda.device(self.device):
+            _expect("n_nodes", n_nodes, (batch,), torch.int32, device)
+        with _on(device):
             if workspace is None:
                 workspace = self._tree_workspaces.get(nodes)
                 if workspace is None:
                     workspace = self._tree_workspaces[nodes] = self.tree_workspace(nodes)
             if out is None:
-                out = torch.empty_like(q)
+                out = torch.empty(q.shape, dtype=bf16, device=device)
             else:
-                _expect("out", out, q.shape, bf16, self.device)
+                _expect("out", out, q.shape, bf16, device)
             kvq_tree_attention(c, self.cache, layer, nodes, q, k_draft, v_draft, mask, n_nodes,
-                               1.0 / math.sqrt(c.head_dim) if softmax_scale is None else softmax_scale, out,
-                               workspace, stream=stream)
+                               1.0 / math.sqrt(D) if softmax_scale is None else softmax_scale, out, workspace,
+                               stream=stream)
         return out
 
     def read(self, layer, first=0, count=None, seq_begin=0, seq_count=None, dtype="bf16", k_out=None, v_out=None,
@@ -161,7 +180,7 @@ class QuantizedKVCache:
         code = {"bf16": KVQ_DTYPE_BF16, "f32": KVQ_DTYPE_F32}[dtype]
         kind = torch.float32 if code == KVQ_DTYPE_F32 else torch.bfloat16
         shape = (seq_count, count, c.kv_heads, c.head_dim)
-        with torch.cuda.device(self.device):
+        with _on(self.device):
             outs = [torch.empty(shape, dtype=kind, device=self.device) if x is None else x for x in (k_out, v_out)]
             _expect("k_out", outs[0], shape, kind, self.device)
             _expect("v_out", outs[1], shape, kind, self.device)
@@ -209,35 +228,38 @@ class RotaryEmbedding:
         projection); positions: int32 [tokens].  Returns (q, k) turned, in new tensors or in
         q_out, k_out (q and k themselves: in place).  transpose: the gradient."""
         import torch
-        given = [(n, x) for n, x in (("q", q), ("k", k)) if x is not None]
-        if not given:
-            raise ValueError("rotate: neither q nor k")
-        dtype, device, tokens = given[0][1].dtype, given[0][1].device, given[0][1].shape[0]
-        if dtype not in (torch.bfloat16, torch.float32) or device.type != "cuda":
-            raise ValueError("rotate: expected bfloat16 or float32 rows on a GPU, got %s on %s" % (dtype, device))
+        x = k if q is None else q
+        if x is None or x.dim() != 3 or x.dtype not in (torch.bfloat16, torch.float32) or not x.is_cuda:
+            raise ValueError("rotate: expected bfloat16 or float32 rows [tokens][heads][head_dim] on a GPU")
+        dtype, device, tokens = x.dtype, x.device, x.shape[0]
         _expect("positions", positions, (tokens,), torch.int32, device)
-        args, outs = [], []
-        with torch.cuda.device(device):
-            for name, x, y in (("q", q, q_out), ("k", k, k_out)):
-                if x is None:
-                    args += [None, None, 0, 0, 0]
-                    outs.append(None)
-                    continue
-                if y is None:
-                    y = torch.empty(x.shape, dtype=dtype, device=device)
-                for n, z in ((name, x), (name + "_out", y)):
-                    self._rows(n, z, x.shape, tokens, dtype, device)
-                args += [x, y, x.shape[1], x.stride(0), y.stride(0)]
-                outs.append(y)
-            kvq_rope(self.rope if dtype == torch.bfloat16 else self._f32, self.frequencies, positions, tokens, *args,
-                     flags=KVQ_ROPE_TRANSPOSE if transpose else 0, stream=stream)
-        return outs[0], outs[1]
+        with _on(device):
+            if q is not None:
+                q_out = self._rows("q", q, q_out, tokens, dtype, device)
+                qa = (q, q_out, q.shape[1], q.stride(0), q_out.stride(0))
+            else:
+                qa, q_out = (None, None, 0, 0, 0), None
+            if k is not None:
+                k_out = self._rows("k", k, k_out, tokens, dtype, device)
+                ka = (k, k_out, k.shape[1], k.stride(0), k_out.stride(0))
+            else:
+                ka, k_out = (None, None, 0, 0, 0), None
+            kvq_rope(self.rope if dtype == torch.bfloat16 else self._f32, self.frequencies, positions, tokens, *qa, *ka,
+                     KVQ_ROPE_TRANSPOSE if transpose else 0, stream)
+        return q_out, k_out
 
-    def _rows(self, name, x, shape, tokens, dtype, device):
+    def _rows(self, name, x, y, tokens, dtype, device):
+        """The output rows for input rows x; refuses what the library would read wrongly."""
+        import torch
         D = self.rope.head_dim
-        if x.dim() != 3 or x.shape != shape or x.shape[0] != tokens or x.shape[2] != D or x.dtype != dtype \
-                or x.device != device:
-            raise ValueError("%s: expected %s [%d][heads][%d] on %s, got %s %s on %s" % (
-                name, dtype, tokens, D, device, x.dtype, tuple(x.shape), x.device))
-        if x.numel() and (x.stride(2) != 1 and D > 1 or x.stride(1) != D and x.shape[1] > 1):
-            raise ValueError("%s: a token's heads must lie one after another" % name)
+        if y is None:
+            y = torch.empty(x.shape, dtype=dtype, device=device)
+        for z in (x, y):
+            if z.dim() != 3 or z.shape != x.shape or z.shape[0] != tokens or z.shape[2] != D or z.dtype != dtype \
+                    or z.device != device:
+                raise ValueError("%s: expected %s [%d][heads][%d] on %s, got %s %s on %s" % (
+                    name, dtype, tokens, D, device, z.dtype, tuple(z.shape), z.device))
+            s = z.stride()
+            if (s[2] != 1 and D > 1 or s[1] != D and z.shape[1] > 1) and z.numel():
+                raise ValueError("%s: a token's heads must lie one after another" % name)
+        return y

@@ -129,6 +129,17 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+def _raw_stream(stream):
+    """_stream, without building a stream object for the current one where torch can tell its
+    handle directly."""
+    if stream is None:
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None:
+            return raw(torch.cuda.current_device())
+    return _stream(stream)
+
+
 def _check(fn, code):
     if code != KVQ_OK:
         raise KvqError(fn, code)
@@ -199,16 +210,20 @@ def kvq_tree_attention(cfg, cache, layer, nodes, q, k_draft, v_draft, mask, n_no
                        workspace_bytes=None, stream=None):
     if workspace_bytes is None:
         workspace_bytes = workspace.numel() * workspace.element_size()
-    _check("kvq_tree_attention", load().kvq_tree_attention(
-        C.byref(cfg), _ptr(cache), int(layer), int(nodes), _ptr(q), _ptr(k_draft), _ptr(v_draft), _ptr(mask),
-        _ptr(n_nodes), float(softmax_scale), _ptr(out), _ptr(workspace), int(workspace_bytes), _stream(stream)))
+    code = (_lib or load()).kvq_tree_attention(
+        C.byref(cfg), _ptr(cache), layer, nodes, _ptr(q), _ptr(k_draft), _ptr(v_draft), _ptr(mask), _ptr(n_nodes),
+        softmax_scale, _ptr(out), _ptr(workspace), workspace_bytes, _raw_stream(stream))
+    if code:
+        raise KvqError("kvq_tree_attention", code)
 
 
 def kvq_read_tokens(cfg, cache, layer, seq_begin, seq_count, starts, first, count, k_out, v_out,
                     out_dtype=KVQ_DTYPE_BF16, stream=None):
-    _check("kvq_read_tokens", load().kvq_read_tokens(
-        C.byref(cfg), _ptr(cache), int(layer), int(seq_begin), int(seq_count), _ptr(starts), int(first), int(count),
-        _ptr(k_out), _ptr(v_out), int(out_dtype), _stream(stream)))
+    code = (_lib or load()).kvq_read_tokens(
+        C.byref(cfg), _ptr(cache), layer, seq_begin, seq_count, _ptr(starts), first, count, _ptr(k_out), _ptr(v_out),
+        out_dtype, _raw_stream(stream))
+    if code:
+        raise KvqError("kvq_read_tokens", code)
 
 
 def kvq_rope_frequencies(rope):
@@ -221,7 +236,8 @@ def kvq_rope_frequencies(rope):
 def kvq_rope(rope, w, positions, tokens, q, q_out, q_heads, q_stride, q_out_stride, k=None, k_out=None, kv_heads=0,
              k_stride=0, k_out_stride=0, flags=0, stream=None):
     """w: ctypes float array (kvq_rope_frequencies); strides in elements."""
-    _check("kvq_rope", load().kvq_rope(
-        C.byref(rope), w, _ptr(positions), int(tokens), _ptr(q), _ptr(q_out), int(q_heads), int(q_stride),
-        int(q_out_stride), _ptr(k), _ptr(k_out), int(kv_heads), int(k_stride), int(k_out_stride), int(flags),
-        _stream(stream)))
+    code = (_lib or load()).kvq_rope(
+        C.byref(rope), w, _ptr(positions), tokens, _ptr(q), _ptr(q_out), q_heads, q_stride, q_out_stride, _ptr(k),
+        _ptr(k_out), kv_heads, k_stride, k_out_stride, flags, _raw_stream(stream))
+    if code:
+        raise KvqError("kvq_rope", code)

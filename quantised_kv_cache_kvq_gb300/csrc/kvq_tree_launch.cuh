@@ -11,10 +11,6 @@ int launch_tree_t(TreeArgs& a, cudaStream_t stream) {
     constexpr int NT = TreeShape<N, D>::kThreads;
     const int64_t smem = TreeShape<N, D>::kStage + (int64_t)a.stages * a.stage_bytes;
     int nb = 0;
-    // as much of the SM's memory as shared memory as there is, for two blocks
-    if (cudaFuncSetAttribute(k_tree<N, D, KIND>, cudaFuncAttributePreferredSharedMemoryCarveout,
-                             cudaSharedmemCarveoutMaxShared) != cudaSuccess)
-        return KVQ_ERR_CUDA;
     const int rc = decode_blocks(reinterpret_cast<const void*>(k_tree<N, D, KIND>), NT, smem, &nb);
     if (rc != KVQ_OK) return rc;
     a.NB = nb < kMaxTreeBlocks ? nb : kMaxTreeBlocks;
