@@ -32,22 +32,25 @@ namespace {
 
 struct TreePlan {
     Layout lo;
-    int N, RT, rows, TT, stages;
+    int N, RT, rows, TT, stages, share, blocks;
+    int stage_at;
     int64_t stage, ml_off, o_off, bytes;
 };
 
 // Bytes of the operand tiles of k_tree<N, D> (TreeShape), and what a block may have next to the
-// kernel's static arrays (under 8 KiB); with two blocks per SM, half of 228 KiB less 1 KiB
-// reserved each and those arrays (under 4 KiB).
+// kernel's static arrays (under 8 KiB); where two blocks share an SM (heads of up to 128
+// channels, up to 64 columns), half of its 228 KiB less 1 KiB reserved and those arrays (under
+// 4.5 KiB).
 int64_t tile_bytes(int N, int D) { return 256 * D + (D > 128 ? 65536 : 32768) + 2 * N * D + 256 * N; }
-constexpr int64_t kTreeSmemLimit = 219 * 1024, kTreeSmemHalf = 109 * 1024;
+constexpr int64_t kTreeSmemLimit = 219 * 1024, kTreeSmemHalf = 108 * 1024 + 512;
 
 // The row tile: the fewest columns, 16 to 128, that hold all queries of a KV head, or 128 (64
 // for heads of 256 channels, whose tiles are twice as large).  The packed bytes of the next two
 // tiles (else the next one) pass through shared memory where they fit next to the operand
-// tiles -- two only if that costs no resident block -- with half the columns if that makes the
-// room; else (KIVI records with many outliers, or of 256 channels at 8 bits) the kernel reads
-// them in place.
+// tiles: two blocks per SM come first, if need be with the weights in the key tile's place (the
+// next keys then wait for their product), then two stages.  Half the columns are taken if that
+// makes the room; else (KIVI records with many outliers, or of 256 channels at 8 bits) the
+// kernel reads them in place.
 int tree_plan(const kvq_config* cfg, int nodes, TreePlan* p) {
     const int rc = make_layout(cfg, cfg->max_tokens, &p->lo);
     if (rc != KVQ_OK) return rc;
@@ -69,9 +72,18 @@ int tree_plan(const kvq_config* cfg, int nodes, TreePlan* p) {
     if (tile_bytes(p->N, D) + p->stage > kTreeSmemLimit && p->N >= 64 &&
         tile_bytes(p->N / 2, D) + p->stage <= kTreeSmemLimit)
         p->N /= 2;
-    const int64_t room = kTreeSmemLimit - tile_bytes(p->N, D);
-    const int64_t half = p->N > 64 || D > 128 ? -1 : kTreeSmemHalf - tile_bytes(p->N, D);
-    p->stages = half >= p->stage ? (half >= 2 * p->stage ? 2 : 1) : room >= 2 * p->stage ? 2 : room >= p->stage ? 1 : 0;
+    const int64_t tiles = tile_bytes(p->N, D), room = kTreeSmemLimit - tiles;
+    p->share = 0;
+    p->blocks = p->N <= 64 && D <= 128 ? 2 : 1;
+    if (p->blocks == 2 && tiles + p->stage > kTreeSmemHalf) {
+        if (p->N <= D && tiles - 256 * p->N + p->stage <= kTreeSmemHalf)
+            p->share = 1;
+        else
+            p->blocks = 1;
+    }
+    const int64_t left = p->blocks == 2 ? kTreeSmemHalf - tiles + (p->share ? 256 * p->N : 0) : room;
+    p->stages = left >= 2 * p->stage ? 2 : left >= p->stage ? 1 : 0;
+    p->stage_at = static_cast<int>(tiles - (p->share ? 256 * p->N : 0));
     if (p->stages == 0) {
         if (lo.scheme != KVQ_SCHEME_KIVI) return KVQ_ERR_UNSUPPORTED;
         p->stage = 0;
@@ -161,6 +173,9 @@ int kvq_tree_attention(const kvq_config* cfg, const void* cache, int32_t layer, 
     a.pieces_inverse = static_cast<uint32_t>((0x100000000ull + a.pieces - 1) / a.pieces);
     for (int i = 0; i < 8; ++i) a.group_of[i] = a.TG > 0 && 16 * i < p.TT ? 16 * i / a.lo.G : 0;
     a.stages = p.stages;
+    a.share = p.share;
+    a.blocks = p.blocks;
+    a.stage_at = p.stage_at;
     a.stage_bytes = static_cast<int>(p.stage);
     a.ml_off = p.ml_off;
     a.o_off = p.o_off;

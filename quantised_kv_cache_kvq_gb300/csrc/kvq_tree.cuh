@@ -46,13 +46,15 @@ struct TreeArgs {
     const uint8_t* cache;
     int layer, nodes, rows, RT;         // rows = nodes * gqa, RT row tiles of N columns
     int gshift;                         // log2 gqa
-    int NB;                             // blocks of the launch
+    int NB, blocks;                     // blocks of the launch, and of an SM
     int TT, TG;                         // tokens, and groups, of a full packed tile
     int gvshift;                        // log2 of the value group (it divides a power of two)
     int pieces;                         // KIVI: pieces of 8 key and value parameters of a group
     uint32_t pieces_inverse;            // 2^32 / pieces, rounded up
     int group_of[8];                    // KIVI: the group of a tile's 16-token piece
     int stages, stage_bytes;            // buffers that a tile's packed bytes pass through (0: none)
+    int share;                          // the weights lie in the key tile (written when its scores are done)
+    int stage_at;                       // where the buffers begin
     const __nv_bfloat16 *q, *k, *v;
     const uint8_t* mask;
     const int32_t* n_nodes;
@@ -1103,7 +1105,7 @@ __global__ void __launch_bounds__(TreeShape<N, D>::kThreads, TreeShape<N, D>::kB
     const int row = 32 * quad + lane;                                   // this thread's token of a tile
     const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
     const int H = lo.H, gqa = lo.gqa, W = key_block(lo);
-    uint8_t *kt = smem + S::kK, *vt = smem + S::kV, *qt = smem + S::kQ, *pt = smem + S::kP, *stage = smem + S::kStage;
+    uint8_t *kt = smem + S::kK, *vt = smem + S::kV, *qt = smem + S::kQ, *pt = smem + (a.share ? S::kK : S::kP), *stage = smem + a.stage_at;
     const bool rope = kivi && lo.rope_base > 0.0f;
     const int row_bytes = lo.scheme == KVQ_SCHEME_INT4 ? D / 2 : D;     // of a code row
 
@@ -1224,6 +1226,7 @@ __global__ void __launch_bounds__(TreeShape<N, D>::kThreads, TreeShape<N, D>::kB
                         __syncthreads();
                     }
                     ++used;
+                    if (a.share) wait(&sh.pv_done, it + 1);             // the weights lie in the key tile
                     bool wide = false;
                     if constexpr (kivi) {
                         wide = kivi_wide<CT>(a, t, tid);
@@ -1251,7 +1254,7 @@ __global__ void __launch_bounds__(TreeShape<N, D>::kThreads, TreeShape<N, D>::kB
                 if (warp == 0 && elect_one()) {
                     tmem_fence_after();
                     const uint64_t dk = mma_desc(smem_addr(kt), D / 8 * kCoreBytes), dq = mma_desc(smem_addr(qt), D / 8 * kCoreBytes);
-#pragma unroll
+#pragma unroll 2
                     for (int k = 0; k < D / 16; ++k)
                         mma_f16(tm_s, dk + k * (2 * kCoreBytes >> 4), dq + k * (2 * kCoreBytes >> 4),
                                 mma_idesc(128, N, false, false), k > 0);
@@ -1402,16 +1405,10 @@ __global__ void __launch_bounds__(TreeShape<N, D>::kThreads, TreeShape<N, D>::kB
 #pragma unroll
                     for (int d = 0; d < S::kDN; ++d) {
                         const uint64_t dv = mma_desc(smem_addr(vt) + d * 32768, 16 * kCoreBytes);
-                        if (steps == 8) {
-#pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                mma_f16(tm_o + d * N, dv + k * (2 * kCoreBytes >> 4), dp + k * (2 * kCoreBytes >> 4), idesc,
-                                        tile > first || k > 0);
-                        } else {
-                            for (int k = 0; k < steps; ++k)
-                                mma_f16(tm_o + d * N, dv + k * (2 * kCoreBytes >> 4), dp + k * (2 * kCoreBytes >> 4), idesc,
-                                        tile > first || k > 0);
-                        }
+#pragma unroll 1
+                        for (int k = 0; k < steps; ++k)
+                            mma_f16(tm_o + d * N, dv + k * (2 * kCoreBytes >> 4), dp + k * (2 * kCoreBytes >> 4), idesc,
+                                    tile > first || k > 0);
                     }
                     mma_commit(&sh.pv_done);
                 }

@@ -9,10 +9,14 @@ namespace kvq {
 template <int N, int D, int KIND>
 int launch_tree_t(TreeArgs& a, cudaStream_t stream) {
     constexpr int NT = TreeShape<N, D>::kThreads;
-    const int64_t smem = TreeShape<N, D>::kStage + (int64_t)a.stages * a.stage_bytes;
+    const int64_t smem = a.stage_at + (int64_t)a.stages * a.stage_bytes;
     int nb = 0;
     const int rc = decode_blocks(reinterpret_cast<const void*>(k_tree<N, D, KIND>), NT, smem, &nb);
     if (rc != KVQ_OK) return rc;
+    // two blocks per SM where the plan left them room (the calculator counts one: it holds the
+    // kernel's tensor memory against it, of which a block takes at most half); blocks do not wait
+    // for each other, so one that is not resident at once costs time only
+    if (a.blocks == 2 && TreeShape<N, D>::kBlocks == 2) nb *= 2;
     a.NB = nb < kMaxTreeBlocks ? nb : kMaxTreeBlocks;
     if (launch_dependent(k_tree<N, D, KIND>, dim3(a.NB), dim3(NT), static_cast<size_t>(smem), stream, a) != cudaSuccess)
         return KVQ_ERR_CUDA;
