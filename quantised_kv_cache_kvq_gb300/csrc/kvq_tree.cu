@@ -34,7 +34,7 @@ struct TreePlan {
     Layout lo;
     int N, RT, rows, TT, stages, share, blocks;
     int stage_at;
-    int64_t stage, ml_off, o_off, bytes;
+    int64_t stage, span_off, ml_off, o_off, bytes;
 };
 
 // Bytes of the operand tiles of k_tree<N, D> (TreeShape), and what a block may have next to the
@@ -90,7 +90,8 @@ int tree_plan(const kvq_config* cfg, int nodes, TreePlan* p) {
     }
     p->RT = (p->rows + p->N - 1) / p->N;
     const int64_t slots = kMaxTreeBlocks + (int64_t)lo.B * lo.H * p->RT;
-    p->ml_off = 256;
+    p->span_off = 256;
+    p->ml_off = align256(p->span_off + (int64_t)lo.B * lo.H * p->RT * 8);
     p->o_off = align256(p->ml_off + slots * p->N * 8);
     p->bytes = align256(p->o_off + slots * p->N * D * 4);
     return KVQ_OK;
@@ -177,6 +178,7 @@ int kvq_tree_attention(const kvq_config* cfg, const void* cache, int32_t layer, 
     a.blocks = p.blocks;
     a.stage_at = p.stage_at;
     a.stage_bytes = static_cast<int>(p.stage);
+    a.span_off = p.span_off;
     a.ml_off = p.ml_off;
     a.o_off = p.o_off;
     if (a.lo.rope_base > 0.0f)

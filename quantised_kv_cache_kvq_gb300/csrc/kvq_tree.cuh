@@ -61,7 +61,7 @@ struct TreeArgs {
     float qscale;                       // softmax scale * log2 e
     __nv_bfloat16* out;
     uint8_t* ws;
-    int64_t ml_off, o_off;              // partials in the workspace: (m, l), then O
+    int64_t span_off, ml_off, o_off;    // in the workspace: each row tile's blocks, partials (m, l), O
     float rope_w[128];
 };
 
@@ -81,10 +81,20 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int b, int N) {
     s.live = ((s.nodes << a.gshift) + N - 1) / N;
     return s;
 }
-// Tiles of all the row tiles of one KV head of a sequence (a row tile without queries is one
+// Cost of the tiles of one row tile, in packed tiles: an unpacked one takes about as long as
+// kRawCost of them (measured).
+constexpr int kRawCost = 3;
+__device__ __forceinline__ int tree_cost(const TreeSeq& s) { return s.packed + (s.tiles - s.packed) * kRawCost; }
+// The first tile that begins at or behind cost position x of a row tile.
+__device__ __forceinline__ int tree_tile_at(const TreeSeq& s, int64_t x) {
+    if (x <= s.packed) return static_cast<int>(x);
+    const int64_t t = s.packed + (x - s.packed + kRawCost - 1) / kRawCost;
+    return t < s.tiles ? static_cast<int>(t) : s.tiles;
+}
+// Cost of all the row tiles of one KV head of a sequence (a row tile without queries is one
 // empty tile: its outputs are set to 0).
 __device__ __forceinline__ int64_t tree_head_tiles(const TreeArgs& a, const TreeSeq& s) {
-    return (int64_t)s.live * s.tiles + (a.RT - s.live);
+    return (int64_t)s.live * tree_cost(s) + (a.RT - s.live);
 }
 
 // Exclusive place of this thread's value in the block's sum, and the sum.
@@ -656,6 +666,21 @@ __device__ __noinline__ void raw_rows(const TreeArgs& a, int b, int h, int n, in
     }
 }
 
+// Rows [r0, r1) of the unpacked ones (the window's part) into L2.
+template <int D, int DT>
+__device__ __noinline__ void prefetch_rows(const TreeArgs& a, int b, int h, int n, int qn, int nodes, int r0, int r1, int tid) {
+    const int window = n - qn, C = a.lo.C, lines = D * 4 / 128;         // of a token's key and value
+    r1 = r1 < window ? r1 : window;
+    if (r0 >= r1) return;
+    const uint8_t* ring = a.cache + a.lo.ring_off + unit_index(a.lo, a.layer, b, h) * C * (int64_t)(4 * D);
+    const uint32_t slot0 = static_cast<uint32_t>(qn) % static_cast<uint32_t>(C);
+    for (int i = r0 * lines + tid; i < r1 * lines; i += DT) {
+        uint32_t slot = slot0 + i / lines;
+        if (slot >= static_cast<uint32_t>(C)) slot -= C;
+        prefetch_l2(ring + (int64_t)slot * (4 * D) + (i % lines) * 128);
+    }
+}
+
 // Turns the tile's cached keys by their positions: row r of the tile is token t0 + (its place),
 // rows from `rows` on stay.
 template <int D, int DT>
@@ -762,43 +787,44 @@ __device__ __forceinline__ int64_t share_start(int64_t total, int64_t j, int64_t
     return total * j / nb;
 }
 // A block's walk over its share of the tiles: segments, each the tiles [first, end) of one row
-// tile of one KV head.
+// tile of one KV head: those that begin in [pos, pos + left) of its cost.
 struct TreeWalk {
     int b, h, rt, first, end, unit_tiles;
     bool live;
     TreeSeq s;
-    int64_t left;
+    int64_t pos, left;
+    __device__ __forceinline__ int64_t unit_cost() const { return live ? tree_cost(s) : 1; }
     __device__ __forceinline__ void segment() {
         live = rt < s.live;
         unit_tiles = live ? s.tiles : 1;
-        end = static_cast<int>(left < unit_tiles - first ? first + left : unit_tiles);
+        const int64_t to = left < unit_cost() - pos ? pos + left : unit_cost();
+        first = live ? tree_tile_at(s, pos) : 0;
+        end = live ? tree_tile_at(s, to) : 1;
     }
-    __device__ __forceinline__ void begin(const TreeArgs& a, int N, int b_, int64_t at, int64_t n) {
+    // the share of `n` from position `at` of sequence b_ on
+    __device__ __forceinline__ void begin(const TreeArgs& a, const TreeSeq& seq, int b_, int64_t at, int64_t n) {
         b = b_;
         left = n;
-        s = tree_seq(a, b, N);
-        const int64_t per = tree_head_tiles(a, s), run = (int64_t)s.live * s.tiles;
+        s = seq;
+        const int64_t per = tree_head_tiles(a, s);
         h = static_cast<int>(at >> 31 ? at / per : static_cast<uint32_t>(at) / static_cast<uint32_t>(per));
-        const int in = static_cast<int>(at - h * per);
-        rt = static_cast<int>(in < run ? in / s.tiles : s.live + (in - run));
-        first = static_cast<int>(in < run ? in % s.tiles : 0);
+        const int in = static_cast<int>(at - h * per), cost = tree_cost(s), run = s.live * cost;
+        rt = in < run ? in / cost : s.live + (in - run);
+        pos = in < run ? in - rt * cost : 0;
         segment();
     }
     // to the next segment; false at the end of the share
     __device__ __forceinline__ bool next(const TreeArgs& a, int N) {
-        left -= end - first;
+        const int64_t took = unit_cost() - pos;
+        left -= took;
         if (left <= 0) return false;
-        if (end < unit_tiles) {
-            first = end;
-        } else {
-            first = 0;
-            if (++rt == a.RT) {
-                rt = 0;
-                if (++h == a.lo.H) {
-                    h = 0;
-                    ++b;
-                    s = tree_seq(a, b, N);
-                }
+        pos = 0;
+        if (++rt == a.RT) {
+            rt = 0;
+            if (++h == a.lo.H) {
+                h = 0;
+                ++b;
+                s = tree_seq(a, b, N);
             }
         }
         segment();
@@ -821,7 +847,7 @@ struct TreeShared {
     float fac[N], part[4][N];       // per column: factors; per quadrant: maxima, sums
     float kf[128], vl[128];         // a raw row's score factor and log2 of its value scale
     float wt[D / 2];                // rotary frequencies in the order of the key tile
-    int64_t scan[32], start[3];
+    int64_t scan[32], start;
     uint64_t stage_full[2], s_full, pv_done;
     const uint8_t* recs[8];         // records read in place
     int qtop, qlow;                 // exponents of the largest and the smallest query
@@ -924,7 +950,12 @@ __device__ __noinline__ void finish_segment(const TreeArgs& a, int first, uint32
     const TreeWalk& w = sh.walk;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = warp & 3, col0 = (warp >> 2) * S::NH;
     const bool whole = first == 0 && w.end == w.unit_tiles;
-    const int64_t slot = blockIdx.x + ((int64_t)w.b * lo.H + w.h) * a.RT + w.rt;
+    const int64_t unit = ((int64_t)w.b * lo.H + w.h) * a.RT + w.rt, slot = blockIdx.x + unit;
+    if (tid == 0) {             // which blocks have a part of the row tile: none to join, or first and last
+        int* span = reinterpret_cast<int*>(a.ws + a.span_off) + 2 * unit;
+        if (first == 0) span[0] = whole ? -1 : static_cast<int>(blockIdx.x);
+        if (w.end == w.unit_tiles) span[1] = static_cast<int>(blockIdx.x);
+    }
     for (int c = tid; c < N; c += S::kThreads) {
         // rows of padding nodes saw the cached tokens with a query of 0: their output is 0
         const float v = w.live && row0 + c < row_end ? (sh.part[0][c] + sh.part[1][c]) + (sh.part[2][c] + sh.part[3][c]) : 0.0f;
@@ -983,6 +1014,16 @@ __device__ __noinline__ void finish_segment(const TreeArgs& a, int first, uint32
             }
         }
     }
+}
+
+// A share that covers only the inside of one tile's cost: a part that the join passes over.
+template <int N, int D>
+__device__ __noinline__ void finish_empty(const TreeArgs& a, TreeShared<N, D>& sh) {
+    const TreeWalk& w = sh.walk;
+    const int64_t slot = blockIdx.x + ((int64_t)w.b * a.lo.H + w.h) * a.RT + w.rt;
+    for (int c = threadIdx.x; c < N; c += TreeShape<N, D>::kThreads)
+        reinterpret_cast<float2*>(a.ws + a.ml_off)[slot * N + c] = make_float2(-INFINITY, 0.0f);
+    __syncthreads();
 }
 
 // A KIVI key tile's further steps: the scaled tile (scaled: always, else where ke != 0), the
@@ -1124,24 +1165,25 @@ __global__ void __launch_bounds__(TreeShape<N, D>::kThreads, TreeShape<N, D>::kB
     grid_launch_dependents();
     // this block's tiles: positions [x0, x1) of all tiles, in the order sequence, KV head, row
     // tile, tile
-    int64_t total, mine = tid < lo.B ? H * tree_head_tiles(a, tree_seq(a, tid, N)) : 0;
+    TreeSeq seq;
+    if (tid < lo.B) seq = tree_seq(a, tid, N);
+    int64_t total, mine = tid < lo.B ? H * tree_head_tiles(a, seq) : 0;
     int64_t at = block_scan<NT>(mine, sh.scan, &total);
     if (lo.B > NT) total = tree_total<NT>(a, N, sh.scan);
     const int64_t nb = total < a.NB ? total : a.NB;     // blocks with a share
     const int64_t x0 = share_start(total, blockIdx.x, nb), x1 = share_start(total, blockIdx.x + 1, nb);
     for (int b0 = 0;;) {
-        if (at <= x0 && x0 < at + mine) {
-            sh.start[0] = b0 + tid;
-            sh.start[1] = x0 - at;
-        }
+        if (at <= x0 && x0 < at + mine && static_cast<int64_t>(blockIdx.x) < nb)
+            sh.walk.begin(a, seq, b0 + tid, x0 - at, x1 - x0);
         if ((b0 += NT) >= lo.B) break;
         const int64_t base = at + mine;                 // of the last thread: the next round's start
-        if (tid == NT - 1) sh.start[2] = base;
+        if (tid == NT - 1) sh.start = base;
         __syncthreads();
         const int b = b0 + tid;
         int64_t sum;
-        mine = b < lo.B ? H * tree_head_tiles(a, tree_seq(a, b, N)) : 0;
-        at = sh.start[2] + block_scan<NT>(mine, sh.scan, &sum);
+        if (b < lo.B) seq = tree_seq(a, b, N);
+        mine = b < lo.B ? H * tree_head_tiles(a, seq) : 0;
+        at = sh.start + block_scan<NT>(mine, sh.scan, &sum);
     }
     tmem_fence_before();
     __syncthreads();
@@ -1163,16 +1205,12 @@ __global__ void __launch_bounds__(TreeShape<N, D>::kThreads, TreeShape<N, D>::kB
         // the walk is kept in shared memory: its fields are needed now and then, and a register
         // that does not hold one of them saves a trip to local memory
         TreeWalk& w = sh.walk;
-        if (tid == 0) {
-            w.begin(a, N, static_cast<int>(sh.start[0]), sh.start[1], x1 - x0);
-            if (staged_tiles) {
-                sh.ahead = w;
-                sh.ahead_slot = 0;
-                copy_unit(a, sh, false);
-                for (int i = 0; i < a.stages; ++i) copy_next<N, D, KIND>(a, sh, stage);
-            }
+        if (staged_tiles && warp == CT / 32 - 1 && elect_one()) {
+            sh.ahead = w;
+            sh.ahead_slot = 0;
+            copy_unit(a, sh, false);
+            for (int i = 0; i < a.stages; ++i) copy_next<N, D, KIND>(a, sh, stage);
         }
-        __syncthreads();
         uint32_t it = 0, used = 0;              // tiles, and packed tiles, so far
         do {
             const int row0 = w.rt * N, row_end = w.s.nodes << a.gshift, first = w.first, end = w.end, packed_end = w.s.packed;
@@ -1182,7 +1220,11 @@ __global__ void __launch_bounds__(TreeShape<N, D>::kThreads, TreeShape<N, D>::kB
             float l[NH];
 #pragma unroll
             for (int i = 0; i < NH; ++i) l[i] = 0.0f;
-            if (live) {
+            if (live && first < end) {
+                // the segment's unpacked rows are needed behind its packed tiles: into L2 meanwhile
+                if (end > packed_end)
+                    prefetch_rows<D, CT>(a, w.b, w.h, w.s.n, w.s.qn, w.s.nodes, (first > packed_end ? first - packed_end : 0) * 128,
+                                         (end - packed_end) * 128, tid);
                 const float2 m = load_queries<N, D>(a, row0, row_end, W, qt, sh);
                 mixed = m.x != 0.0f;
                 gscale = m.y;
@@ -1415,6 +1457,9 @@ __global__ void __launch_bounds__(TreeShape<N, D>::kThreads, TreeShape<N, D>::kB
                 __syncwarp();
             }
             // ---------------------------------------------------------- the segment's result
+            if (live && first >= end) {         // none of the unit's tiles begins in this share
+                finish_empty<N, D>(a, sh);
+            } else {
             if (live) wait(&sh.pv_done, it + 1);
             tmem_fence_after();
             // the sums over a column's tokens, through the key tile's memory: [column][token]
@@ -1433,6 +1478,7 @@ __global__ void __launch_bounds__(TreeShape<N, D>::kThreads, TreeShape<N, D>::kB
             tmem_fence_before();
             __syncthreads();
             tmem_fence_after();
+            }
             if (tid == 0) sh.more = w.next(a, N);
             __syncthreads();
         } while (sh.more);
@@ -1444,67 +1490,80 @@ __global__ void __launch_bounds__(TreeShape<N, D>::kThreads, TreeShape<N, D>::kB
     if (warp == 0) tmem_free(tm_s, S::kCols);
 }
 
-// Joins the partial results of row tiles that several blocks worked on.  A block takes CW
-// columns of one row tile: it finds the blocks whose shares meet the row tile's tiles, and for
-// each column sums their O 2^(m - M) and l 2^(m - M).
+// Joins the partial results of row tiles that several blocks worked on: a block takes 4 columns
+// of one row tile, weighs the blocks' parts by 2^(m - M) and sums their O and l.
+constexpr int kMergeColumns = 4;
 template <int N, int D>
 __global__ void __launch_bounds__(kMergeThreads) k_tree_merge(const __grid_constant__ TreeArgs a) {
-    constexpr int CW = N < 32 ? N / 2 : 16;
-    __shared__ int64_t scan[8], start;
+    constexpr int CW = kMergeColumns, QUADS = CW * D / 4, GROUPS = kMergeThreads / QUADS;
+    __shared__ float2 part[kMaxTreeBlocks * CW];        // (m, l), then (weight, -)
+    __shared__ float sum[CW];
+    __shared__ float4 red[GROUPS > 1 ? kMergeThreads : 1];
     const Layout& lo = a.lo;
-    const int64_t unit = blockIdx.x / (N / CW);
-    const int c0 = static_cast<int>(blockIdx.x % (N / CW)) * CW;
-    const int rt = static_cast<int>(unit % a.RT);
-    const int64_t bh = unit / a.RT;
-    const int b = static_cast<int>(bh / lo.H), h = static_cast<int>(bh % lo.H);
-    const int row0 = rt * N;
-    // the token counts are not written by the attention: the plan needs no wait for it
-    const int64_t total = tree_total<kMergeThreads>(a, N, scan);
-    int64_t base = 0;
-    for (int b0 = 0; b0 <= b; b0 += kMergeThreads) {
-        const int bb = b0 + threadIdx.x;
-        int64_t sum;
-        const int64_t at = base + block_scan<kMergeThreads>(bb < lo.B ? lo.H * tree_head_tiles(a, tree_seq(a, bb, N)) : 0, scan, &sum);
-        if (bb == b) start = at;
-        base += sum;
-    }
-    __syncthreads();
-    const TreeSeq s = tree_seq(a, b, N);
-    const int64_t nb = total < a.NB ? total : a.NB;
-    const int64_t y0 = start + h * tree_head_tiles(a, s) + (int64_t)rt * s.tiles, y1 = y0 + s.tiles;
-    // block j has the positions [total j / nb, total (j + 1) / nb)
-    int64_t j0 = y0 * nb / total, j1;
-    while (share_start(total, j0 + 1, nb) <= y0) ++j0;
-    while (share_start(total, j0, nb) > y0) --j0;
-    for (j1 = j0; share_start(total, j1 + 1, nb) < y1;) ++j1;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int unit = blockIdx.x / (N / CW), c0 = (blockIdx.x % (N / CW)) * CW;
+    const int rt = unit % a.RT, bh = unit / a.RT, b = bh / lo.H, h = bh - b * lo.H, row0 = rt * N + c0;
     // every block waits, also one with nothing to join: the launch after this one may rely on it
     grid_dependency_wait();
-    if (rt >= s.live || j0 == j1) return;
-    const float2* ml = reinterpret_cast<const float2*>(a.ws + a.ml_off);
-    const float* po = reinterpret_cast<const float*>(a.ws + a.o_off);
-    for (int i = threadIdx.x; i < CW * D; i += kMergeThreads) {
-        const int c = c0 + i / D, ch = i % D, r = row0 + c;
-        if (r >= a.rows) continue;
-        float M = -INFINITY;
-        for (int64_t j = j0; j <= j1; ++j) {
-            const float2 x = ml[(j + unit) * N + c];
-            if (x.y != 0.0f) M = fmaxf(M, x.x);
-        }
-        float L = 0.0f, O = 0.0f;
-        for (int64_t j = j0; j <= j1; ++j) {
-            const float2 x = ml[(j + unit) * N + c];
-            const float o = po[((j + unit) * N + c) * D + ch];
-            if (x.y == 0.0f) {
-                if (!(fabsf(o) < INFINITY)) O += o;     // a visible draft's value that is not finite
-                continue;
-            }
-            const float f = tree_exp2(x.x - M);
+    const int2 span = reinterpret_cast<const int2*>(a.ws + a.span_off)[unit];
+    if (span.x < 0 || row0 >= a.rows) return;
+    const int J = span.y - span.x + 1;
+    const int64_t slot0 = (int64_t)span.x + unit;
+    const float2* ml = reinterpret_cast<const float2*>(a.ws + a.ml_off) + slot0 * N + c0;
+    for (int i = tid; i < J * CW; i += kMergeThreads) part[i] = ml[(int64_t)(i / CW) * N + i % CW];
+    __syncthreads();
+    if (warp < CW) {
+        float M = -INFINITY, L = 0.0f;
+        for (int j = lane; j < J; j += 32)
+            if (part[j * CW + warp].y != 0.0f) M = fmaxf(M, part[j * CW + warp].x);
+        M = warp_max(M);
+        for (int j = lane; j < J; j += 32) {
+            const float2 x = part[j * CW + warp];
+            const float f = x.y != 0.0f ? tree_exp2(x.x - M) : 0.0f;
             L = fmaf(x.y, f, L);
-            O += fabsf(o) < INFINITY ? o * f : o;
+            // a negative weight: nothing was written for this part
+            part[j * CW + warp].x = x.x == -INFINITY ? -1.0f : f;
         }
-        a.out[(((int64_t)b * a.nodes + (r >> a.gshift)) * lo.Hq + h * lo.gqa + (r & (lo.gqa - 1))) * D + ch] =
-            __float2bfloat16_rn(L != 0.0f ? O / L : 0.0f);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+        if (lane == 0) sum[warp] = L != 0.0f ? 1.0f / L : 0.0f;
     }
+    __syncthreads();
+    const int quad = tid % QUADS, group = tid / QUADS, c = quad / (D / 4);
+    const float4* po = reinterpret_cast<const float4*>(a.ws + a.o_off) + slot0 * (N * D / 4) + c0 * (D / 4) + quad;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    // (a value that is not finite -- a visible draft's -- goes through unweighted)
+    auto add = [](float& s, float x, float f) { s += fabsf(x) < INFINITY ? x * f : x; };
+#pragma unroll 4
+    for (int j = group; j < J; j += GROUPS) {
+        const float f = part[j * CW + c].x;
+        if (f < 0.0f) continue;
+        const float4 x = po[(int64_t)j * (N * D / 4)];
+        add(o.x, x.x, f);
+        add(o.y, x.y, f);
+        add(o.z, x.z, f);
+        add(o.w, x.w, f);
+    }
+    if constexpr (GROUPS > 1) {
+        red[tid] = o;
+        __syncthreads();
+        if (group > 0) return;
+        for (int g = 1; g < GROUPS; ++g) {
+            const float4 x = red[g * QUADS + quad];
+            o.x += x.x;
+            o.y += x.y;
+            o.z += x.z;
+            o.w += x.w;
+        }
+    }
+    const int r = row0 + c;
+    if (r >= a.rows) return;
+    const float f = sum[c];
+    auto out = [&](float x) { return fabsf(x) < INFINITY ? x * f : x; };
+    __nv_bfloat162 lo2 = __floats2bfloat162_rn(out(o.x), out(o.y)), hi2 = __floats2bfloat162_rn(out(o.z), out(o.w));
+    *reinterpret_cast<uint2*>(a.out + (((int64_t)b * a.nodes + (r >> a.gshift)) * lo.Hq + h * lo.gqa + (r & (lo.gqa - 1))) * D +
+                              4 * (quad % (D / 4))) =
+        make_uint2(*reinterpret_cast<uint32_t*>(&lo2), *reinterpret_cast<uint32_t*>(&hi2));
 }
 
 }  // namespace kvq

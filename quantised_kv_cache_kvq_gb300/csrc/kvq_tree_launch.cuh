@@ -21,8 +21,7 @@ int launch_tree_t(TreeArgs& a, cudaStream_t stream) {
     if (launch_dependent(k_tree<N, D, KIND>, dim3(a.NB), dim3(NT), static_cast<size_t>(smem), stream, a) != cudaSuccess)
         return KVQ_ERR_CUDA;
     const int64_t units = (int64_t)a.lo.B * a.lo.H * a.RT;
-    constexpr int CW = N < 32 ? N / 2 : 16;
-    return launch_dependent(k_tree_merge<N, D>, dim3(static_cast<unsigned>(units * (N / CW))), dim3(kMergeThreads), 0, stream,
+    return launch_dependent(k_tree_merge<N, D>, dim3(static_cast<unsigned>(units * (N / kMergeColumns))), dim3(kMergeThreads), 0, stream,
                             a) == cudaSuccess
                ? KVQ_OK
                : KVQ_ERR_CUDA;
