@@ -37,9 +37,13 @@ namespace kvq {
 
 constexpr int kMergeThreads = 256;
 constexpr int kMaxTreeBlocks = 608;     // of a launch: bounds the workspace's partial results
-constexpr float kNoMax = -1.0e30f;      // reference of a column that has seen nothing
 constexpr float kHead = 8.0f;           // P of the largest entry, log2
 constexpr float kReach = 15.0f;         // P may grow to 2^15 before the reference moves
+
+// What a kernel unpacks: KIVI records of 2, 4 or 8 bits, KIVI records read where they lie (any
+// bits; those that do not fit next to the operand tiles), INT8 and INT4 rows, FP8 tiles.  The
+// kinds are kernels of their own: together in one, their code costs every role registers.
+enum TreeKind { kKivi2 = 2, kKivi4 = 4, kKivi8 = 8, kInPlace = 16, kRows = 32, kFp8 = 64 };
 
 struct TreeArgs {
     Layout lo;
@@ -596,22 +600,30 @@ __device__ __forceinline__ void load_words(const uint16_t* p, uint32_t (&w)[8]) 
     w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w; w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
 }
 
+// The channels' order as a compile-time number where the kind fixes it (else -1).
+template <int KIND>
+__device__ __forceinline__ constexpr int fixed_block() {
+    return KIND <= kKivi8 ? 32 / KIND : KIND == kFp8 ? 0 : -1;
+}
+
 // bf16 rows (the window's tokens, then the drafts) [r0, r0 + cnt) of unit (b, h): keys and
 // values into their tiles, with their powers of two.  A warp takes an octet of rows, a lane 16
-// channels of one row at a time; each row is scaled by its own largest element.  *bad: a
-// draft's value is not finite (it is 0 in the tile).
-template <int D, int DT>
-__device__ __noinline__ void raw_rows(const TreeArgs& a, int b, int h, int n, int qn, int r0, int cnt, int W, bool paired_values,
-                                      uint8_t* kt, uint8_t* vt, float* kf, float* vlog, int* bad, int tid) {
-    constexpr int UNITS = D / 16, STEPS = (UNITS + 3) / 4;
+// channels of one row at a time; each row is scaled by its own largest element (the second
+// loads hit the cache).  *bad: a draft's value is not finite (it is 0 in the tile).  The loops
+// are not unrolled: what runs once or twice in a block costs its instructions' fetch first.
+template <int D, int DT, int KIND>
+__device__ __noinline__ void raw_rows(const TreeArgs& a, int b, int h, int n, int qn, int r0, int cnt, uint8_t* kt, uint8_t* vt,
+                                      float* kf, float* vlog, int* bad, int tid) {
+    constexpr int UNITS = D / 16, STEPS = (UNITS + 3) / 4, WK = fixed_block<KIND>();
+    const int W = WK >= 0 ? WK : key_block(a.lo);
     const int warp = tid >> 5, lane = tid & 31, window = n - qn, C = a.lo.C;
     const uint32_t slot0 = C > 0 ? static_cast<uint32_t>(qn) % static_cast<uint32_t>(C) : 0u;
     const uint16_t* ring = reinterpret_cast<const uint16_t*>(a.cache + a.lo.ring_off) + unit_index(a.lo, a.layer, b, h) * C * (2 * D);
     const int64_t draft0 = (((int64_t)b * a.nodes - window) * a.lo.H + h) * D;      // row r: + r H D
+#pragma unroll 1
     for (int o = warp; o < 16; o += DT / 32) {
         const int row = 8 * o + (lane & 7), r = r0 + row;
         if ((8 * o & ~15) >= cnt) break;
-        uint32_t w[2][STEPS][8];
         const uint16_t *kp = nullptr, *vp = nullptr;
         if (row < cnt) {
             if (r < window) {
@@ -625,37 +637,56 @@ __device__ __noinline__ void raw_rows(const TreeArgs& a, int b, int h, int n, in
                 vp = reinterpret_cast<const uint16_t*>(a.v) + at;
             }
         }
+        const bool draft = r >= window;
+        uint32_t ktop = 0, vtop = 0;
 #pragma unroll
         for (int i = 0; i < STEPS; ++i) {
             const int unit = (lane >> 3) + 4 * i;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) w[0][i][j] = w[1][i][j] = 0u;
-            if (kp && unit < UNITS) {
-                load_words(kp + 16 * unit, w[0][i]);
-                load_words(vp + 16 * unit, w[1][i]);
-            }
+            if (!kp || unit >= UNITS) continue;
+            uint32_t x[8], y[8];
+            load_words(kp + 16 * unit, x);
+            load_words(vp + 16 * unit, y);
+            ktop = max(ktop, unit_top(x));
+            vtop = max(vtop, unit_top(y));
         }
-        const bool draft = r >= window;
-#pragma unroll
+#pragma unroll 1
         for (int kv = 0; kv < 2; ++kv) {
-            bool odd = false;
-            const int e = range_exponent(row_top(w[kv], kv == 0 || !draft, &odd));
-            if (kv && odd && draft) *bad = 1;
+            const uint16_t* p = kv ? vp : kp;
+            uint32_t top = kv ? vtop : ktop;
+            const bool odd = top >= 0x7f80u, clear = kv && draft;
+            uint32_t w[8];
+            if (odd) {
+                top = 0;
+                for (int unit = lane >> 3; unit < UNITS; unit += 4) {
+                    load_words(p + 16 * unit, w);
+                    top = max(top, finite_top(w, true));
+                }
+                if (clear) *bad = 1;
+            }
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 8));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
+            const int e = range_exponent(__uint_as_float(top << 16));
             const float f = pow2i(-e);
+#pragma unroll 1
+            for (int unit = lane >> 3; unit < UNITS; unit += 4) {
 #pragma unroll
-            for (int i = 0; i < STEPS; ++i) {
-                const int unit = (lane >> 3) + 4 * i;
-                if (unit >= UNITS) continue;
+                for (int j = 0; j < 8; ++j) w[j] = 0u;
+                if (p) load_words(p + 16 * unit, w);
+                if (odd && clear) finite_top(w, false);
                 uint32_t hw[8];
-                half_words(w[kv][i], f, hw);
+                half_words(w, f, hw);
                 if (kv == 0) {
                     store_unit<D>(kt, row, unit, hw, W);
                 } else {
-                    uint32_t pw[8];
-                    pair_words(hw, paired_values ? W : 0, pw);
+                    if (KIND == kRows) {
+                        pair_words(hw, W, w);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) w[j] = hw[j];
+                    }
                     uint8_t* at = vt + (row >> 3) * kCoreBytes + (row & 7) * 16 + 2 * unit * 16 * kCoreBytes;
-                    *reinterpret_cast<uint4*>(at) = make_uint4(pw[0], pw[1], pw[2], pw[3]);
-                    *reinterpret_cast<uint4*>(at + 16 * kCoreBytes) = make_uint4(pw[4], pw[5], pw[6], pw[7]);
+                    *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+                    *reinterpret_cast<uint4*>(at + 16 * kCoreBytes) = make_uint4(w[4], w[5], w[6], w[7]);
                 }
             }
             if (lane < 8) {
@@ -710,11 +741,6 @@ __device__ __noinline__ void turn_keys(uint8_t* kt, const float* w, int64_t t0, 
         *pb = make_uint4(oy[0], oy[1], oy[2], oy[3]);
     }
 }
-
-// What a kernel unpacks: KIVI records of 2, 4 or 8 bits, KIVI records read where they lie (any
-// bits; those that do not fit next to the operand tiles), INT8 and INT4 rows, FP8 tiles.  The
-// kinds are kernels of their own: together in one, their code costs every role registers.
-enum TreeKind { kKivi2 = 2, kKivi4 = 4, kKivi8 = 8, kInPlace = 16, kRows = 32, kFp8 = 64 };
 
 // Shapes of an instantiation: N columns, D channels.
 template <int N, int D>
@@ -844,6 +870,7 @@ struct TreeWalk {
 template <int N, int D>
 struct TreeShared {
     float colg[N], colr[N];         // a column's query scale and minus its reference
+    int seen[N];                    // it has a reference
     float fac[N], part[4][N];       // per column: factors; per quadrant: maxima, sums
     float kf[128], vl[128];         // a raw row's score factor and log2 of its value scale
     float wt[D / 2];                // rotary frequencies in the order of the key tile
@@ -883,10 +910,12 @@ __device__ __forceinline__ float warp_max(float x) {
 // below it keeps binary16's subnormal steps, 2^-39 of the largest.  Where one is smaller
 // still, each gets a power of its own, and the scores their columns' factors.  Returns (such
 // factors are needed, the factor of all scores); ends behind a block barrier.
-template <int N, int D>
-__device__ __noinline__ float2 load_queries(const TreeArgs& a, int row0, int row_end, int W, uint8_t* qt,
+template <int N, int D, int KIND>
+__device__ __noinline__ float2 load_queries(const TreeArgs& a, int row0, int row_end, uint8_t* qt,
                                             TreeShared<N, D>& sh) {
     const TreeWalk& w = sh.walk;
+    constexpr int WK = fixed_block<KIND>();
+    const int W = WK >= 0 ? WK : key_block(a.lo);
     constexpr int UNITS = D / 16, STEPS = (UNITS + 3) / 4, WARPS = TreeShape<N, D>::kThreads / 32;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gqa = a.lo.gqa;
     if (tid == 0) {
@@ -932,7 +961,8 @@ __device__ __noinline__ float2 load_queries(const TreeArgs& a, int row0, int row
         }
         if (lane < 8) {
             sh.colg[c] = a.qscale * pow2i(e);
-            sh.colr[c] = -kNoMax;
+            sh.colr[c] = 0.0f;
+            sh.seen[c] = 0;
         }
     }
     __syncthreads();
@@ -1145,7 +1175,8 @@ __global__ void __launch_bounds__(TreeShape<N, D>::kThreads, TreeShape<N, D>::kB
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, quad = warp & 3, col0 = (warp >> 2) * NH;
     const int row = 32 * quad + lane;                                   // this thread's token of a tile
     const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
-    const int H = lo.H, gqa = lo.gqa, W = key_block(lo);
+    constexpr int WK = fixed_block<KIND>();
+    const int H = lo.H, W = WK >= 0 ? WK : key_block(lo);
     uint8_t *kt = smem + S::kK, *vt = smem + S::kV, *qt = smem + S::kQ, *pt = smem + (a.share ? S::kK : S::kP), *stage = smem + a.stage_at;
     const bool rope = kivi && lo.rope_base > 0.0f;
     const int row_bytes = lo.scheme == KVQ_SCHEME_INT4 ? D / 2 : D;     // of a code row
@@ -1225,10 +1256,11 @@ __global__ void __launch_bounds__(TreeShape<N, D>::kThreads, TreeShape<N, D>::kB
                 if (end > packed_end)
                     prefetch_rows<D, CT>(a, w.b, w.h, w.s.n, w.s.qn, w.s.nodes, (first > packed_end ? first - packed_end : 0) * 128,
                                          (end - packed_end) * 128, tid);
-                const float2 m = load_queries<N, D>(a, row0, row_end, W, qt, sh);
+                const float2 m = load_queries<N, D, KIND>(a, row0, row_end, qt, sh);
                 mixed = m.x != 0.0f;
                 gscale = m.y;
             }
+            bool seen_cached = false;           // a tile with cached tokens is behind us
             for (int tile = first; live && tile < end; ++tile, ++it) {
                 const bool packed = tile < packed_end;
                 const int cnt = packed ? w.packed_count(a, tile) : w.raw_count(tile);
@@ -1244,7 +1276,7 @@ __global__ void __launch_bounds__(TreeShape<N, D>::kThreads, TreeShape<N, D>::kB
                 if (!packed) {
                     const int r0 = (tile - w.s.packed) * 128, held = w.s.n - w.s.qn - r0;
                     wait(&sh.pv_done, it + 1);                          // the rows write both tiles
-                    raw_rows<D, CT>(a, w.b, w.h, w.s.n, w.s.qn, r0, cnt, W, rows_scheme, kt, vt, sh.kf, sh.vl, &sh.odd, tid);
+                    raw_rows<D, CT, KIND>(a, w.b, w.h, w.s.n, w.s.qn, r0, cnt, kt, vt, sh.kf, sh.vl, &sh.odd, tid);
                     if (rope) {
                         __syncthreads();
                         turn_keys<D, CT>(kt, sh.wt, (int64_t)w.s.qn + r0, held < cnt ? held : cnt, false, tid);
@@ -1348,51 +1380,48 @@ __global__ void __launch_bounds__(TreeShape<N, D>::kThreads, TreeShape<N, D>::kB
                 // ---- softmax
                 const float inv = tree_exp2(-lv);
                 const uint64_t f2 = pack2(f, f), lv2 = pack2(lv, lv), inv2 = pack2(inv, inv);
-                const uint8_t* mask = a.mask ? a.mask + (int64_t)w.b * a.nodes * a.nodes : nullptr;
-                // x + log2 s of B columns from c0 on, less the references if REF
-                auto scores = [&](int c0, float (&x)[B], bool ref) {
-                    tmem_load(my_s + c0, x);
+                // which columns see this token
+                uint32_t sees = valid ? 0xffffffffu : 0u;
+                if (draft >= 0) {
+                    const uint8_t* mask = a.mask ? a.mask + (int64_t)w.b * a.nodes * a.nodes + draft : nullptr;
+                    sees = 0u;
+#pragma unroll 1
+                    for (int i = 0; i < B; ++i) {
+                        const int r = row0 + col0 + i, node = r >> a.gshift;
+                        if (r < row_end && (mask ? mask[node * a.nodes] != 0 : draft <= node)) sees |= 1u << i;
+                    }
+                }
+                wait(&sh.s_full, it);
+                tmem_fence_after();
+                // x = score + log2 s, less the column's reference.  Until a column has one, which it
+                // surely has behind a tile with cached tokens, the references are set first
+                bool fresh = tile == first || (!packed && !seen_cached);
+                seen_cached |= packed || (tile - packed_end) * 128 < w.s.n - w.s.qn;
+                float x[B];
+                for (;;) {
+                    tmem_load(my_s, x);
                     if (mixed) {
 #pragma unroll
-                        for (int i = 0; i < B; ++i) x[i] *= sh.colg[col0 + c0 + i];
+                        for (int i = 0; i < B; ++i) x[i] *= sh.colg[col0 + i];
                     }
 #pragma unroll
                     for (int i = 0; i < B; i += 4) {
-                        uint64_t u = fma2(pack2(x[i], x[i + 1]), f2, lv2), v = fma2(pack2(x[i + 2], x[i + 3]), f2, lv2);
-                        if (ref) {
-                            const ulonglong2 r = *reinterpret_cast<const ulonglong2*>(&sh.colr[col0 + c0 + i]);
-                            u = add2(u, r.x);
-                            v = add2(v, r.y);
-                        }
+                        const ulonglong2 r = *reinterpret_cast<const ulonglong2*>(&sh.colr[col0 + i]);
+                        const uint64_t u = add2(fma2(pack2(x[i], x[i + 1]), f2, lv2), r.x);
+                        const uint64_t v = add2(fma2(pack2(x[i + 2], x[i + 3]), f2, lv2), r.y);
                         unpack2(u, &x[i], &x[i + 1]);
                         unpack2(v, &x[i + 2], &x[i + 3]);
                     }
                     if (masked) {
 #pragma unroll
-                        for (int i = 0; i < B; ++i) {
-                            bool see = valid;
-                            if (draft >= 0) {
-                                const int r = row0 + col0 + c0 + i, node = r >> a.gshift;
-                                see = r < row_end && (mask ? mask[node * a.nodes + draft] != 0 : draft <= node);
-                            }
-                            x[i] = see ? x[i] : -INFINITY;
-                        }
+                        for (int i = 0; i < B; ++i) x[i] = sees >> i & 1u ? x[i] : -INFINITY;
                     }
-                };
-                wait(&sh.s_full, it);
-                tmem_fence_after();
-                float x[B];
-                float hi = kNoMax;
-                scores(0, x, true);
+                    float hi = -INFINITY;
 #pragma unroll
-                for (int i = 0; i < B; i += 2) hi = max3(hi, x[i], x[i + 1]);
-                const bool over = __syncthreads_or(hi > kReach);
-                // behind the barrier the tile's packed bytes are read: the next ones may come
-                if (staged_tiles && packed && warp == CT / 32 - 1 && elect_one()) copy_next<N, D, KIND>(a, sh, stage);
-                if (over) {
+                    for (int i = 0; i < B; i += 2) hi = max3(hi, x[i], x[i + 1]);
+                    if (!__syncthreads_or(fresh || hi > kReach)) break;
                     // the columns' maxima over the tile, the new references, and everything so far
                     // under them
-                    scores(0, x, false);
 #pragma unroll
                     for (int i = 0; i < B; ++i) {
                         const float m = warp_max(x[i]);
@@ -1400,13 +1429,15 @@ __global__ void __launch_bounds__(TreeShape<N, D>::kThreads, TreeShape<N, D>::kB
                     }
                     __syncthreads();
                     for (int c = tid; c < N; c += CT) {
-                        const float m = fmaxf(fmaxf(sh.part[0][c], sh.part[1][c]), fmaxf(sh.part[2][c], sh.part[3][c])) - kHead;
-                        const float old = -sh.colr[c], now = fmaxf(old, m);
+                        const float top = fmaxf(fmaxf(sh.part[0][c], sh.part[1][c]), fmaxf(sh.part[2][c], sh.part[3][c]));
+                        const float old = -sh.colr[c], m = top + old - kHead;
+                        const bool had = sh.seen[c] != 0, any = top > -INFINITY;
+                        const float now = any ? (had ? fmaxf(old, m) : m) : old;
+                        sh.seen[c] = had || any;
                         sh.colr[c] = -now;
-                        sh.fac[c] = tree_exp2(old - now);
+                        sh.fac[c] = had ? tree_exp2(old - now) : 1.0f;
                     }
                     __syncthreads();
-                    scores(0, x, true);
                     if (tile > first) {
 #pragma unroll
                         for (int i = 0; i < NH; ++i) l[i] *= sh.fac[col0 + i];
@@ -1422,7 +1453,10 @@ __global__ void __launch_bounds__(TreeShape<N, D>::kThreads, TreeShape<N, D>::kB
                                 tmem_store(at, o);
                             }
                     }
+                    fresh = false;
                 }
+                // behind the barrier the tile's packed bytes are read: the next ones may come
+                if (staged_tiles && packed && warp == CT / 32 - 1 && elect_one()) copy_next<N, D, KIND>(a, sh, stage);
                 uint8_t* prow = pt + (row >> 3) * kCoreBytes + (row & 7) * 16;
 #pragma unroll
                 for (int c = 0; c < B; c += 8) {
