@@ -266,7 +266,7 @@ __device__ __forceinline__ void kivi_keys(const TreeArgs& a, const Tile t, uint8
     const int unit = (warp % QUADS) * 4 + (((lane >> 3) + lane) & 3), o0 = (warp / QUADS) * PER;
     uint32_t s[8], z[8];
     int have = -1;
-#pragma unroll 2
+#pragma unroll 4
     for (int o = o0; o < o0 + PER; ++o) {
         const int row = 8 * o + (lane & 7), tok = packed_token(row);
         if (8 * (o & ~1) >= t.cnt) break;
@@ -350,6 +350,16 @@ __device__ __forceinline__ void kivi_values(const TreeArgs& args, const Tile t, 
     }
 }
 
+// Largest magnitude in the tile's side lists (as bf16 << 16), over a thread's share.
+template <int DT, typename Tile>
+__device__ __noinline__ uint32_t side_wide(const Layout& lo, const Tile t, int tid) {
+    uint32_t top = 0;
+    for (int g = 0; g * lo.G < t.cnt; ++g) {
+        const uint32_t* side = reinterpret_cast<const uint32_t*>(t.rec(g) + lo.kc + lo.vc + lo.kp + lo.vp);
+        for (int i = tid; i < (lo.ko + lo.vo) / 4; i += DT) top = max(top, side[i] & 0x7fff0000u);
+    }
+    return top;
+}
 // Whether some |value| that the tile's keys or values can have reaches 2^15, over a thread's
 // share of their parameters (in binary16: levels * s + |z|, an infinity counts).  Piece i of 8
 // parameters of a tile lies `piece` bytes into its group's record.
@@ -370,11 +380,7 @@ __device__ __forceinline__ bool kivi_wide(const TreeArgs& a, const Tile& t, int 
 #pragma unroll
         for (int j = 0; j < 4; ++j) top = __hmax2(top, __hfma2(levels, u32_as_h2(sw[j]), __habs2(u32_as_h2(zw[j]))));
     }
-    if (lo.K > 0)
-        for (int g = 0; g * lo.G < t.cnt; ++g) {
-            const uint32_t* side = reinterpret_cast<const uint32_t*>(t.rec(g) + lo.kc + lo.vc + lo.kp + lo.vp);
-            for (int i = tid; i < (lo.ko + lo.vo) / 4; i += DT) side_top = max(side_top, side[i] & 0x7fff0000u);
-        }
+    if (lo.K > 0) side_top = side_wide<DT>(lo, t, tid);
     const uint32_t h = h2_as_u32(top);
     return (h & 0xffffu) >= 0x7800u || (h >> 16) >= 0x7800u || side_top >= 0x47000000u;
 }
@@ -469,6 +475,7 @@ __device__ __forceinline__ void fp8_16(const uint4& v, bool e4m3, uint32_t (&o)[
 template <int D, int DT>
 __device__ __forceinline__ void fp8_keys(const uint8_t* codes, int cnt, bool e4m3, uint8_t* kt, int tid) {
     constexpr uint32_t sbo = D / 8 * kCoreBytes;
+#pragma unroll 4
     for (int i = tid; i < 128 * D / 16; i += DT) {
         const int row = (i & 7) + 8 * (i / (D / 2)), unit = ((i >> 3) + row) % (D / 16), tok = packed_token(row);
         if ((row & ~15) >= cnt) break;
@@ -480,6 +487,7 @@ __device__ __forceinline__ void fp8_keys(const uint8_t* codes, int cnt, bool e4m
 }
 template <int D, int DT>
 __device__ __forceinline__ void fp8_values(const uint8_t* codes, int cnt, bool e4m3, bool negative, uint8_t* vt, int tid) {
+#pragma unroll 4
     for (int i = tid; i < 8 * D; i += DT) {
         const int c = i % D, a = i / D;
         if (16 * a >= cnt) break;
@@ -503,6 +511,7 @@ __device__ __forceinline__ void fp8_values(const uint8_t* codes, int cnt, bool e
 // weights); keys K-major, values with their channels inside a row (MN-major).
 template <int D, int DT>
 __device__ __forceinline__ void rows_codes(const uint8_t* codes, int cnt, int kv, bool int8, uint8_t* tile, int tid) {
+#pragma unroll 4
     for (int i = tid; i < 128 * D / 16; i += DT) {
         const int row = (i & 7) + 8 * (i / (D / 2)), unit = ((i >> 3) + row) % (D / 16);
         if ((row & ~15) >= cnt) break;
@@ -724,21 +733,17 @@ __device__ __noinline__ void turn_keys(uint8_t* kt, const float* w, int64_t t0, 
         if (tok >= rows) continue;
         uint4* pa = reinterpret_cast<uint4*>(kt + core_at(row, ch, sbo));
         uint4* pb = reinterpret_cast<uint4*>(kt + core_at(row, ch + CH, sbo));
-        const uint4 va = *pa, vb = *pb;
-        const uint32_t x[4] = {va.x, va.y, va.z, va.w}, y[4] = {vb.x, vb.y, vb.z, vb.w};
-        uint32_t ox[4], oy[4];
         const float pos = static_cast<float>(t0 + tok);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float2 fx = __half22float2(u32_as_h2(x[j])), fy = __half22float2(u32_as_h2(y[j]));
-            float s0, c0, s1, c1;
-            rope_sincos(__fmul_rn(pos, w[8 * ch + 2 * j]), &s0, &c0);
-            rope_sincos(__fmul_rn(pos, w[8 * ch + 2 * j + 1]), &s1, &c1);
-            ox[j] = h2_as_u32(__floats2half2_rn(fx.x * c0 - fy.x * s0, fx.y * c1 - fy.y * s1));
-            oy[j] = h2_as_u32(__floats2half2_rn(fy.x * c0 + fx.x * s0, fy.y * c1 + fx.y * s1));
+#pragma unroll 1
+        for (int j = 0; j < 8; ++j) {           // (one sine's code, not eight)
+            __half* px = reinterpret_cast<__half*>(pa) + j;
+            __half* py = reinterpret_cast<__half*>(pb) + j;
+            const float x = __half2float(*px), y = __half2float(*py);
+            float sn, cs;
+            rope_sincos(__fmul_rn(pos, w[8 * ch + j]), &sn, &cs);
+            *px = __float2half_rn(x * cs - y * sn);
+            *py = __float2half_rn(y * cs + x * sn);
         }
-        *pa = make_uint4(ox[0], ox[1], ox[2], ox[3]);
-        *pb = make_uint4(oy[0], oy[1], oy[2], oy[3]);
     }
 }
 
@@ -881,10 +886,11 @@ struct TreeShared {
     uint32_t tmem, top[2];
     TreeWalk walk;                  // the segment
     int more;
-    // the next packed tile to bring in: its segment, the unit's packed bytes and groups
+    // the next packed tile to bring in: its segment, where it lies, what is left of the segment's
+    // packed part (KIVI: groups; others: tokens), its first group
     TreeWalk ahead;
-    const uint8_t* ahead_base;
-    int ahead_tile, ahead_end, ahead_groups;
+    const uint8_t* ahead_src;
+    int ahead_left, ahead_group;
     uint32_t ahead_slot;
     int dead, odd;                  // a wait gave up; a draft's value is not finite
 };
@@ -1085,78 +1091,86 @@ __device__ __noinline__ void kivi_exponents(const Layout& lo, const Tile t, uint
     __syncthreads();
 }
 
-// The unit that sh.ahead is in, for copy_next; to the next unit with packed tiles where it has
+// The segment that sh.ahead is in, for copy_next; the next one with packed tiles where it has
 // none left (`on`).  One thread.
-template <int N, int D>
-__device__ __noinline__ void copy_unit(const TreeArgs& a, TreeShared<N, D>& sh, bool on) {
+template <int N, int D, int KIND>
+__device__ __noinline__ void copy_segment(const TreeArgs& a, TreeShared<N, D>& sh, bool on) {
     TreeWalk& w = sh.ahead;
-    for (;;) {
+    for (;; on = true) {
         if (on && !w.next(a, N)) {
-            sh.ahead_tile = sh.ahead_end = 0;
-            w.left = 0;
+            sh.ahead_left = -1;         // nothing more
             return;
         }
-        on = true;
         const int end = w.live ? (w.end < w.s.packed ? w.end : w.s.packed) : 0;
         if (w.first >= end) continue;
-        sh.ahead_tile = w.first;
-        sh.ahead_end = end;
-        sh.ahead_groups = a.TG > 0 ? w.s.qn / a.lo.G : 0;
-        sh.ahead_base = a.cache + a.lo.data_off + unit_index(a.lo, a.layer, w.b, w.h) * a.lo.unit;
+        const uint8_t* base = a.cache + a.lo.data_off + unit_index(a.lo, a.layer, w.b, w.h) * a.lo.unit;
+        const int all = w.s.qn < end * a.TT ? w.s.qn : end * a.TT, rest = all - w.first * a.TT;
+        if constexpr (KIND <= kInPlace) {
+            sh.ahead_group = w.first * a.TG;
+            sh.ahead_left = rest / a.lo.G;
+            sh.ahead_src = base + (int64_t)sh.ahead_group * a.lo.rec;
+        } else {
+            sh.ahead_left = rest;
+            sh.ahead_src = base + (int64_t)w.first * 128 * (a.lo.scheme == KVQ_SCHEME_INT4 ? D / 2 : D);
+        }
         return;
+    }
+}
+// `ng` group records from the pages that sh.ahead's block table names.
+template <int N, int D>
+__device__ __noinline__ void copy_pages(const TreeArgs& a, TreeShared<N, D>& sh, uint8_t* to, uint64_t* bar, int ng) {
+    const Layout& lo = a.lo;
+    const int32_t* table = lo.table + (int64_t)sh.ahead.b * lo.MP;
+    int pg = sh.ahead_group / lo.PG, in = sh.ahead_group - pg * lo.PG;
+    for (int g = 0; g < ng; ++g) {
+        int32_t page = table[pg];
+        if (page < 0 || page >= lo.NP) {        // outside the pool: page 0 in its place, reported
+            atomicOr(reinterpret_cast<uint32_t*>(a.ws), KVQ_STATUS_BAD_PAGE);
+            page = 0;
+        }
+        bulk_copy_g2s(to + g * lo.rec,
+                      a.cache + lo.data_off + (int64_t)page * lo.page + (((int64_t)a.layer * lo.H + sh.ahead.h) * lo.PG + in) * lo.rec,
+                      lo.rec, bar);
+        if (++in == lo.PG) {
+            in = 0;
+            ++pg;
+        }
     }
 }
 // Brings the block's next packed tile, if there is one, to the next stage; one thread.
 template <int N, int D, int KIND>
 __device__ __forceinline__ void copy_next(const TreeArgs& a, TreeShared<N, D>& sh, uint8_t* stage) {
-    constexpr bool rows_scheme = KIND == kRows;
     const Layout& lo = a.lo;
-    if (sh.ahead_tile >= sh.ahead_end) {
-        if (sh.ahead.left <= 0) return;
-        copy_unit(a, sh, true);
-        if (sh.ahead_tile >= sh.ahead_end) return;
-    }
-    if (*static_cast<volatile int*>(&sh.dead)) return;
-    const int tile = sh.ahead_tile;
+    if (sh.ahead_left == 0) copy_segment<N, D, KIND>(a, sh, true);
+    const int left = sh.ahead_left;
+    if (left <= 0 || *static_cast<volatile int*>(&sh.dead)) return;
     const uint32_t slot = sh.ahead_slot;
-    sh.ahead_tile = tile + 1;
     if (a.stages == 2) sh.ahead_slot = slot ^ 1;
     uint8_t* to = stage + slot * a.stage_bytes;
     uint64_t* bar = &sh.stage_full[slot];
+    const uint8_t* src = sh.ahead_src;
     if constexpr (KIND <= kInPlace) {
-        const int g0 = tile * a.TG, rest = sh.ahead_groups - g0, ng = rest < a.TG ? rest : a.TG;
+        const int ng = left < a.TG ? left : a.TG;
+        sh.ahead_left = left - ng;
+        sh.ahead_src = src + a.TG * lo.rec;
         mbar_arrive_expect_tx(bar, static_cast<uint32_t>(ng * lo.rec));
-        if (lo.PG == 0) {
-            bulk_copy_g2s(to, sh.ahead_base + (int64_t)g0 * lo.rec, ng * lo.rec, bar);
-        } else {
-            const TreeWalk& w = sh.ahead;
-            const int32_t* table = lo.table + (int64_t)w.b * lo.MP;
-            int pg = g0 / lo.PG, in = g0 - pg * lo.PG;
-            for (int g = 0; g < ng; ++g) {
-                int32_t page = table[pg];
-                if (page < 0 || page >= lo.NP) {        // outside the pool: page 0 in its place, reported
-                    atomicOr(reinterpret_cast<uint32_t*>(a.ws), KVQ_STATUS_BAD_PAGE);
-                    page = 0;
-                }
-                bulk_copy_g2s(to + g * lo.rec,
-                              a.cache + lo.data_off + (int64_t)page * lo.page + (((int64_t)a.layer * lo.H + w.h) * lo.PG + in) * lo.rec,
-                              lo.rec, bar);
-                if (++in == lo.PG) {
-                    in = 0;
-                    ++pg;
-                }
-            }
-        }
+        if (lo.PG == 0)
+            bulk_copy_g2s(to, src, ng * lo.rec, bar);
+        else
+            copy_pages(a, sh, to, bar, ng);
+        sh.ahead_group += a.TG;
     } else {
+        const int cnt = left < 128 ? left : 128, c16 = (cnt + 15) & ~15;
         const int row_bytes = lo.scheme == KVQ_SCHEME_INT4 ? D / 2 : D;
-        const int cnt = sh.ahead.packed_count(a, tile), c16 = (cnt + 15) & ~15;
-        const uint8_t* src = sh.ahead_base + (int64_t)tile * (128 * row_bytes);
+        sh.ahead_left = left - cnt;
+        sh.ahead_src = src + 128 * row_bytes;
         const uint32_t bytes = static_cast<uint32_t>(c16 * row_bytes);
-        mbar_arrive_expect_tx(bar, 2 * bytes + (rows_scheme ? 8 * c16 : 0));
+        mbar_arrive_expect_tx(bar, 2 * bytes + (KIND == kRows ? 8 * c16 : 0));
         bulk_copy_g2s(to, src, bytes, bar);
         bulk_copy_g2s(to + 128 * row_bytes, src + (int64_t)lo.T16 * row_bytes, bytes, bar);
-        if (rows_scheme) {
-            const uint8_t* sc = sh.ahead_base + 2 * (int64_t)lo.T16 * row_bytes + 512 * (int64_t)tile;
+        if constexpr (KIND == kRows) {          // the scales: 4 bytes a row from the unit's codes' end on
+            const uint8_t* base = a.cache + lo.data_off + unit_index(lo, a.layer, sh.ahead.b, sh.ahead.h) * lo.unit;
+            const uint8_t* sc = base + 2 * (int64_t)lo.T16 * row_bytes + (src - base) / row_bytes * 4;
             bulk_copy_g2s(to + 256 * row_bytes, sc, 4 * c16, bar);
             bulk_copy_g2s(to + 256 * row_bytes + 512, sc + 4 * (int64_t)lo.T16, 4 * c16, bar);
         }
@@ -1239,7 +1253,7 @@ __global__ void __launch_bounds__(TreeShape<N, D>::kThreads, TreeShape<N, D>::kB
         if (staged_tiles && warp == CT / 32 - 1 && elect_one()) {
             sh.ahead = w;
             sh.ahead_slot = 0;
-            copy_unit(a, sh, false);
+            copy_segment<N, D, KIND>(a, sh, false);
             for (int i = 0; i < a.stages; ++i) copy_next<N, D, KIND>(a, sh, stage);
         }
         uint32_t it = 0, used = 0;              // tiles, and packed tiles, so far
@@ -1386,9 +1400,16 @@ __global__ void __launch_bounds__(TreeShape<N, D>::kThreads, TreeShape<N, D>::kB
                     const uint8_t* mask = a.mask ? a.mask + (int64_t)w.b * a.nodes * a.nodes + draft : nullptr;
                     sees = 0u;
 #pragma unroll 1
-                    for (int i = 0; i < B; ++i) {
-                        const int r = row0 + col0 + i, node = r >> a.gshift;
-                        if (r < row_end && (mask ? mask[node * a.nodes] != 0 : draft <= node)) sees |= 1u << i;
+                    for (int c = 0; c < B; c += 8) {        // 8 loads on their way at a time
+                        uint32_t bits = 0u;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int r = row0 + col0 + c + i, node = r >> a.gshift;
+                            const bool in = r < row_end;
+                            const uint32_t byte = mask ? (in ? mask[node * a.nodes] : 0u) : (in && draft <= node ? 1u : 0u);
+                            bits |= (byte != 0u ? 1u : 0u) << i;
+                        }
+                        sees |= bits << c;
                     }
                 }
                 wait(&sh.s_full, it);
@@ -1455,8 +1476,6 @@ __global__ void __launch_bounds__(TreeShape<N, D>::kThreads, TreeShape<N, D>::kB
                     }
                     fresh = false;
                 }
-                // behind the barrier the tile's packed bytes are read: the next ones may come
-                if (staged_tiles && packed && warp == CT / 32 - 1 && elect_one()) copy_next<N, D, KIND>(a, sh, stage);
                 uint8_t* prow = pt + (row >> 3) * kCoreBytes + (row & 7) * 16;
 #pragma unroll
                 for (int c = 0; c < B; c += 8) {
@@ -1469,6 +1488,8 @@ __global__ void __launch_bounds__(TreeShape<N, D>::kThreads, TreeShape<N, D>::kB
                     }
                     *reinterpret_cast<uint4*>(prow + ((col0 + c) >> 3) * (16 * kCoreBytes)) = make_uint4(p[0], p[1], p[2], p[3]);
                 }
+                // behind the vote's barrier the tile's packed bytes are read: the next ones may come
+                if (staged_tiles && packed && warp == CT / 32 - 1 && elect_one()) copy_next<N, D, KIND>(a, sh, stage);
                 smem_to_async();
                 tmem_fence_before();
                 __syncthreads();
