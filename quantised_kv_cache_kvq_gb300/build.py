@@ -64,7 +64,6 @@ UNITS = {
     "kvq_tree_kivi2_d128.cu": [],
     "kvq_tree_kivi4_d128.cu": [],
     "kvq_tree_kivi8_d128.cu": [],
-    "kvq_tree_inplace_d128.cu": [],
     "kvq_tree_rows_d128.cu": [],
     "kvq_tree_fp8_d128.cu": [],
     "kvq_tree_kivi2_d256.cu": [],

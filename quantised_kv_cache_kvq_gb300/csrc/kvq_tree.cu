@@ -18,7 +18,6 @@ int launch_tree_fp8_d64(TreeArgs& a, int N, cudaStream_t stream);
 int launch_tree_kivi2_d128(TreeArgs& a, int N, cudaStream_t stream);
 int launch_tree_kivi4_d128(TreeArgs& a, int N, cudaStream_t stream);
 int launch_tree_kivi8_d128(TreeArgs& a, int N, cudaStream_t stream);
-int launch_tree_inplace_d128(TreeArgs& a, int N, cudaStream_t stream);
 int launch_tree_rows_d128(TreeArgs& a, int N, cudaStream_t stream);
 int launch_tree_fp8_d128(TreeArgs& a, int N, cudaStream_t stream);
 int launch_tree_kivi2_d256(TreeArgs& a, int N, cudaStream_t stream);
@@ -48,9 +47,9 @@ constexpr int64_t kTreeSmemLimit = 219 * 1024, kTreeSmemHalf = 108 * 1024 + 512;
 // for heads of 256 channels, whose tiles are twice as large).  The packed bytes of the next two
 // tiles (else the next one) pass through shared memory where they fit next to the operand
 // tiles: two blocks per SM come first, if need be with the weights in the key tile's place (the
-// next keys then wait for their product), then two stages.  Half the columns are taken if that
-// makes the room; else (KIVI records with many outliers, or of 256 channels at 8 bits) the
-// kernel reads them in place.
+// next keys then wait for their product), then two stages.  Fewer columns are taken if that makes
+// the room; else (KIVI records of 256 channels at 8 bits or with many outliers) the kernel reads
+// them in place.
 int tree_plan(const kvq_config* cfg, int nodes, TreePlan* p) {
     const int rc = make_layout(cfg, cfg->max_tokens, &p->lo);
     if (rc != KVQ_OK) return rc;
@@ -69,9 +68,8 @@ int tree_plan(const kvq_config* cfg, int nodes, TreePlan* p) {
         p->stage = lo.scheme == KVQ_SCHEME_INT8 ? 256 * D + 1024 : lo.scheme == KVQ_SCHEME_INT4 ? 128 * D + 1024 : 256 * D;
     }
     p->stage = (p->stage + 127) / 128 * 128;
-    if (tile_bytes(p->N, D) + p->stage > kTreeSmemLimit && p->N >= 64 &&
-        tile_bytes(p->N / 2, D) + p->stage <= kTreeSmemLimit)
-        p->N /= 2;
+    if (tile_bytes(16, D) + p->stage <= kTreeSmemLimit)
+        while (tile_bytes(p->N, D) + p->stage > kTreeSmemLimit) p->N /= 2;
     const int64_t tiles = tile_bytes(p->N, D), room = kTreeSmemLimit - tiles;
     p->share = 0;
     p->blocks = p->N <= 64 && D <= 128 ? 2 : 1;
@@ -106,8 +104,7 @@ int launch_tree(TreeArgs& a, int N, cudaStream_t st) {
         return D == 32 ? launch_tree_fp8_d32(a, N, st) : D == 64 ? launch_tree_fp8_d64(a, N, st)
              : D == 128 ? launch_tree_fp8_d128(a, N, st) : launch_tree_fp8_d256(a, N, st);
     if (a.stages == 0)
-        return D == 128 ? launch_tree_inplace_d128(a, N, st) : D == 256 ? launch_tree_inplace_d256(a, N, st)
-                                                                        : KVQ_ERR_UNSUPPORTED;
+        return D == 256 ? launch_tree_inplace_d256(a, N, st) : KVQ_ERR_UNSUPPORTED;
     switch (a.lo.bits) {
         case 2:
             return D == 64 ? launch_tree_kivi2_d64(a, N, st) : D == 128 ? launch_tree_kivi2_d128(a, N, st)

@@ -1342,7 +1342,7 @@ __global__ void __launch_bounds__(TreeShape<N, D>::kThreads, TreeShape<N, D>::kB
                 if (warp == 0 && elect_one()) {
                     tmem_fence_after();
                     const uint64_t dk = mma_desc(smem_addr(kt), D / 8 * kCoreBytes), dq = mma_desc(smem_addr(qt), D / 8 * kCoreBytes);
-#pragma unroll 2
+#pragma unroll
                     for (int k = 0; k < D / 16; ++k)
                         mma_f16(tm_s, dk + k * (2 * kCoreBytes >> 4), dq + k * (2 * kCoreBytes >> 4),
                                 mma_idesc(128, N, false, false), k > 0);
@@ -1476,6 +1476,9 @@ __global__ void __launch_bounds__(TreeShape<N, D>::kThreads, TreeShape<N, D>::kB
                     }
                     fresh = false;
                 }
+                // behind the vote's barrier the tile's packed bytes are read: the next ones may come
+                if (staged_tiles && packed && warp == CT / 32 - 1 && elect_one()) copy_next<N, D, KIND>(a, sh, stage);
+                __syncwarp();
                 uint8_t* prow = pt + (row >> 3) * kCoreBytes + (row & 7) * 16;
 #pragma unroll
                 for (int c = 0; c < B; c += 8) {
@@ -1488,12 +1491,10 @@ __global__ void __launch_bounds__(TreeShape<N, D>::kThreads, TreeShape<N, D>::kB
                     }
                     *reinterpret_cast<uint4*>(prow + ((col0 + c) >> 3) * (16 * kCoreBytes)) = make_uint4(p[0], p[1], p[2], p[3]);
                 }
-                // behind the vote's barrier the tile's packed bytes are read: the next ones may come
-                if (staged_tiles && packed && warp == CT / 32 - 1 && elect_one()) copy_next<N, D, KIND>(a, sh, stage);
                 smem_to_async();
                 tmem_fence_before();
                 __syncthreads();
-                if (warp == 0 && elect_one()) {
+                if (warp == CT / 32 - 2 && elect_one()) {       // (not the warp that issued the scores)
                     tmem_fence_after();
                     const uint64_t dp = mma_desc(smem_addr(pt), 16 * kCoreBytes);
                     const int steps = (cnt + 15) >> 4;
@@ -1502,7 +1503,7 @@ __global__ void __launch_bounds__(TreeShape<N, D>::kThreads, TreeShape<N, D>::kB
 #pragma unroll
                     for (int d = 0; d < S::kDN; ++d) {
                         const uint64_t dv = mma_desc(smem_addr(vt) + d * 32768, 16 * kCoreBytes);
-#pragma unroll 1
+#pragma unroll 4
                         for (int k = 0; k < steps; ++k)
                             mma_f16(tm_o + d * N, dv + k * (2 * kCoreBytes >> 4), dp + k * (2 * kCoreBytes >> 4), idesc,
                                     tile > first || k > 0);

@@ -83,6 +83,9 @@ CACHES = [
     dict(bits=8, group_k=16, group_v=16, head_dim=128, outliers=4, lengths=(150,), max_tokens=160, residual=5),
     dict(bits=4, group_k=64, group_v=32, rope_base=10000.0, lengths=(280, 65), max_tokens=300),
     dict(bits=2, group_k=32, group_v=32, rope_base=500000.0, outliers=1, lengths=(270, 3), max_tokens=300, paged=1),
+    dict(bits=2, group_k=16, group_v=16, head_dim=256, outliers=3, lengths=(150, 40), max_tokens=160, residual=5, q_heads=4, paged=2),
+    dict(bits=4, group_k=16, group_v=16, head_dim=256, outliers=2, lengths=(100,), max_tokens=160, residual=0, rope_base=10000.0,
+         q_heads=8),
     dict(scheme="int8", head_dim=32, lengths=(257, 128, 0), max_tokens=300),
     dict(scheme="int8", head_dim=256, lengths=(129, 16), max_tokens=130, q_heads=2),
     dict(scheme="int4", head_dim=64, lengths=(300, 2), max_tokens=301),
@@ -365,6 +368,57 @@ def test_tree_split_contexts(K):
     """One long context over many blocks beside empty and short ones."""
     p, gen = make(dict(bits=2, lengths=(6000, 0, 33), max_tokens=6016, kv_heads=1, q_heads=4))
     check_tree(K, p, *drafts(p, 5, gen), nodes=[5, 5, 0])
+
+
+@pytest.mark.parametrize("gqa,nodes", [(1, 3), (8, 40)])
+def test_tree_of_more_sequences_than_threads(K, gqa, nodes):
+    gen = torch.Generator().manual_seed(4)
+    lengths = torch.randint(0, 40, (600,), generator=gen).tolist()
+    p, gen = make(dict(bits=2, head_dim=64, kv_heads=1, q_heads=gqa, lengths=lengths, max_tokens=64, residual=8))
+    counts = torch.randint(-1, nodes + 3, (600,), generator=gen).tolist()      # out of range: as the nearest in it
+    q, dk, dv, mask = drafts(p, nodes, gen)
+    cache = wrap(K, p)
+    got = cache.tree_decode(0, q.cuda(), dk.cuda(), dv.cuda(), mask.cuda(),
+                            torch.tensor(counts, dtype=torch.int32, device="cuda")).float().cpu().numpy()
+    some = [0, 255, 256, 257, 511, 512, 598, 599] + list(range(100, 130))
+    few = [min(max(c, 0), nodes) if b in some else 0 for b, c in enumerate(counts)]
+    ref, tol = tree64(p, 0, q, dk, dv, mask.numpy(), few, 0.125)
+    assert (np.abs(got - ref) <= tol)[some].all()
+    for b, c in enumerate(counts):
+        assert not got[b, max(c, 0):].any()
+
+
+def test_tree_replayed_over_a_growing_cache(K):
+    p, gen = make(dict(bits=4, lengths=(250, 60), max_tokens=900))
+    cache = wrap(K, p)
+    q, dk, dv, mask = drafts(p, 6, gen)
+    args = [x.cuda() for x in (q, dk, dv, mask)]
+    ws, out = cache.tree_workspace(6), torch.zeros(q.shape, dtype=BF16, device="cuda")
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        cache.tree_decode(0, *args, out=out, workspace=ws)
+    for n in (1, 300, 17):
+        p.append(0, *p.rand_kv(2, n, gen))
+        g.replay()
+        torch.cuda.synchronize()
+        ref, tol = tree64(p, 0, q, dk, dv, mask.numpy(), None, 1.0 / math.sqrt(128))
+        assert (np.abs(out.float().cpu().numpy() - ref) <= tol).all()
+
+
+def test_tree_queries_of_very_different_sizes(K):
+    """A query far larger than the others, or not finite, changes nothing for them."""
+    p, gen = make(dict(bits=2, lengths=(200, 64), max_tokens=208))
+    q, dk, dv, mask = drafts(p, 9, gen)
+    clean = check_tree(K, p, q, dk, dv, mask)
+    for big in (1e30, math.inf, math.nan):
+        q2 = q.clone()
+        q2[:, 4] *= big
+        got = wrap(K, p).tree_decode(0, q2.cuda(), dk.cuda(), dv.cuda(), mask.cuda()).float().cpu().numpy()
+        ref, tol = tree64(p, 0, q, dk, dv, mask.numpy(), None, 1.0 / math.sqrt(128))
+        others = [i for i in range(9) if i != 4]
+        assert (np.abs(got - ref) <= tol)[:, others].all()
+    assert np.isfinite(clean).all()
 
 
 def test_tree_is_repeatable_and_captured(K):
