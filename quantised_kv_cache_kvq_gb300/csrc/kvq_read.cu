@@ -20,8 +20,6 @@
 namespace kvq {
 namespace {
 
-constexpr int kReadThreads = 128;
-
 struct ReadArgs {
     Layout lo;
     uint8_t* cache;
@@ -86,7 +84,7 @@ struct Rows {
 };
 
 // One KIVI group: tokens t0 .. of record `rec`.
-template <int BITS, typename T>
+template <int BITS, int NT, typename T>
 __device__ __forceinline__ void read_group(const ReadArgs& a, const uint8_t* rec, int t0, const Rows<T>& o) {
     const Layout& lo = a.lo;
     const int D = lo.D, G = lo.G, units = D / 16, ushift = a.dshift - 4;
@@ -96,7 +94,7 @@ __device__ __forceinline__ void read_group(const ReadArgs& a, const uint8_t* rec
         float s[16], z[16];
         halves16(rec + lo.kc + lo.vc + 32 * u, s);
         halves16(rec + lo.kc + lo.vc + 2 * D + 32 * u, z);
-        for (int i = threadIdx.x >> ushift; i < G; i += kReadThreads >> ushift) {
+        for (int i = threadIdx.x >> ushift; i < G; i += NT >> ushift) {
             const int t = t0 + i;
             if (t < o.lo || t >= o.hi) continue;
             const uint32_t* src = reinterpret_cast<const uint32_t*>(rec + (i * D + 16 * u) * BITS / 8);
@@ -116,7 +114,7 @@ __device__ __forceinline__ void read_group(const ReadArgs& a, const uint8_t* rec
         // channels 16 q + g + 8 r of tokens 2 i + s and 2 i + s + 8
         constexpr int HW = 16 / BITS;
         const int wpl = D * BITS / 64, sw = wpl < 4 ? wpl : 4;
-        for (int it = threadIdx.x; it < G / 2 * units; it += kReadThreads) {
+        for (int it = threadIdx.x; it < G / 2 * units; it += NT) {
             const int q = it & (units - 1), pair = it >> ushift, piece = pair >> 3, tt = pair & 7;
             const int ta = t0 + 16 * piece + tt;
             const bool wa = ta >= o.lo && ta < o.hi, wb = ta + 8 >= o.lo && ta + 8 < o.hi;
@@ -146,13 +144,13 @@ __device__ __forceinline__ void read_group(const ReadArgs& a, const uint8_t* rec
         __syncthreads();
         const uint32_t* side = reinterpret_cast<const uint32_t*>(rec + lo.kc + lo.vc + lo.kp + lo.vp);
         if (o.out[0])
-            for (int i = threadIdx.x; i < lo.K * D; i += kReadThreads) {
+            for (int i = threadIdx.x; i < lo.K * D; i += NT) {
                 const uint32_t e = side[i];
                 const int t = t0 + static_cast<int>(e & 0xffffu);
                 if (t >= o.lo && t < o.hi) store1(o.at(0, t, i & (D - 1)), __uint_as_float(e & 0xffff0000u));
             }
         if (o.out[1])
-            for (int i = threadIdx.x; i < lo.K * lo.NGv * G; i += kReadThreads) {
+            for (int i = threadIdx.x; i < lo.K * lo.NGv * G; i += NT) {
                 const uint32_t e = side[lo.K * D + i];
                 const int at = i % (lo.NGv * G), in = at % G, tt = in & 15;
                 const int t = t0 + in - tt + (tt >> 1) + 8 * (tt & 1);
@@ -163,10 +161,10 @@ __device__ __forceinline__ void read_group(const ReadArgs& a, const uint8_t* rec
 }
 
 // bf16 rows of the KIVI window, tokens [max(lo, first), hi): token t in slot t mod C.
-template <typename T>
+template <int NT, typename T>
 __device__ __forceinline__ void read_window(const ReadArgs& a, const uint8_t* ring, int n, const Rows<T>& o) {
     const int D = a.lo.D, units = D / 16, ushift = a.dshift - 4;
-    for (int it = threadIdx.x; it < (o.hi - o.lo) * 2 * units; it += kReadThreads) {
+    for (int it = threadIdx.x; it < (o.hi - o.lo) * 2 * units; it += NT) {
         const int u = it & (units - 1), kv = (it >> ushift) & 1, t = o.lo + (it >> (ushift + 1));
         if (!o.out[kv]) continue;
         float x[16] = {};
@@ -185,22 +183,22 @@ __device__ __forceinline__ void read_window(const ReadArgs& a, const uint8_t* ri
 }
 
 // Rows of the tokens that the cache does not hold: 0.
-template <typename T>
+template <int NT, typename T>
 __device__ __forceinline__ void zero_rows(const ReadArgs& a, const Rows<T>& o) {
     const int units = a.lo.D / 16, ushift = a.dshift - 4;
     const float x[16] = {};
-    for (int it = threadIdx.x; it < (o.hi - o.lo) * 2 * units; it += kReadThreads) {
+    for (int it = threadIdx.x; it < (o.hi - o.lo) * 2 * units; it += NT) {
         const int kv = (it >> ushift) & 1;
         if (o.out[kv]) store16(o.at(kv, o.lo + (it >> (ushift + 1)), 16 * (it & (units - 1))), x);
     }
 }
 
 // INT8 or INT4 rows.
-template <bool INT8, typename T>
+template <bool INT8, int NT, typename T>
 __device__ __forceinline__ void read_rows(const ReadArgs& a, const uint8_t* base, const Rows<T>& o) {
     const int D = a.lo.D, units = D / 16, ushift = a.dshift - 4;
     const int64_t width = INT8 ? D : D / 2;
-    for (int it = threadIdx.x; it < (o.hi - o.lo) * 2 * units; it += kReadThreads) {
+    for (int it = threadIdx.x; it < (o.hi - o.lo) * 2 * units; it += NT) {
         const int u = it & (units - 1), kv = (it >> ushift) & 1, t = o.lo + (it >> (ushift + 1));
         if (!o.out[kv]) continue;
         const uint8_t* src = base + ((int64_t)kv * a.lo.T16 + t) * width + u * (INT8 ? 16 : 8);
@@ -225,13 +223,13 @@ __device__ __forceinline__ void read_rows(const ReadArgs& a, const uint8_t* base
 
 // FP8 tiles: key rows in quarters (channels 2i, 2i + 1, 2i + 8, 2i + 9 of block kb at byte 4 kb
 // of quarter i), values [channel][16 tokens] per tile, token tt at byte 2 (tt mod 8) + tt / 8.
-template <typename T>
+template <int NT, typename T>
 __device__ __forceinline__ void read_fp8(const ReadArgs& a, const uint8_t* base, const float* scales, const Rows<T>& o) {
     const int D = a.lo.D, units = D / 16, ushift = a.dshift - 4;
     const bool e4m3 = a.lo.scheme == KVQ_SCHEME_FP8_E4M3;
     if (o.out[0]) {
         const float s = scales[0];
-        for (int it = threadIdx.x; it < (o.hi - o.lo) * units; it += kReadThreads) {
+        for (int it = threadIdx.x; it < (o.hi - o.lo) * units; it += NT) {
             const int u = it & (units - 1), t = o.lo + (it >> ushift);
             float x[16];
 #pragma unroll
@@ -249,7 +247,7 @@ __device__ __forceinline__ void read_fp8(const ReadArgs& a, const uint8_t* base,
         const float s = scales[1];
         const uint8_t* vbase = base + (int64_t)a.lo.T16 * D;
         const int quads = D / 4, qshift = a.dshift - 2, p0 = o.lo >> 4, pieces = ((o.hi - 1) >> 4) - p0 + 1;
-        for (int it = threadIdx.x; it < pieces * 4 * quads; it += kReadThreads) {
+        for (int it = threadIdx.x; it < pieces * 4 * quads; it += NT) {
             const int q = it & (quads - 1), k = (it >> qshift) & 3, piece = p0 + (it >> (qshift + 2));
             const uint8_t* src = vbase + (int64_t)piece * 16 * D + 64 * q + 4 * k;      // bytes 4 k .. of channels 4 q ..
             uint32_t w[4];
@@ -268,8 +266,8 @@ __device__ __forceinline__ void read_fp8(const ReadArgs& a, const uint8_t* base,
     }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kReadThreads) k_read(const __grid_constant__ ReadArgs a) {
+template <typename T, int NT>
+__global__ void __launch_bounds__(NT) k_read(const __grid_constant__ ReadArgs a) {
     const Layout& lo = a.lo;
     const int bi = blockIdx.z, b = a.seq_begin + bi, h = blockIdx.y;
     const int32_t* st = state_ptr(lo, a.cache, a.layer, b);
@@ -296,35 +294,35 @@ __global__ void __launch_bounds__(kReadThreads) k_read(const __grid_constant__ R
     for (int kv = 0; kv < 2; ++kv)
         o.out[kv] = a.out[kv] ? static_cast<T*>(a.out[kv]) + ((int64_t)bi * a.count + shift - first) * a.row + (int64_t)h * lo.D : nullptr;
     if (shift != 0 || to <= 0 || from >= n) {
-        zero_rows(a, o);
+        zero_rows<NT>(a, o);
         return;
     }
     if (lo.scheme == KVQ_SCHEME_KIVI) {
         if (t0 >= qn) {
-            read_window(a, a.cache + lo.ring_off + unit_index(lo, a.layer, b, h) * lo.C * (int64_t)(4 * lo.D), n, o);
+            read_window<NT>(a, a.cache + lo.ring_off + unit_index(lo, a.layer, b, h) * lo.C * (int64_t)(4 * lo.D), n, o);
             return;
         }
         const int64_t off = group_offset(lo, a.layer, b, h, t0 / lo.G);
         if (off < 0) {                          // a table entry outside the pool
             if (threadIdx.x == 0) atomicOr(reinterpret_cast<uint32_t*>(a.cache), KVQ_STATUS_BAD_PAGE);
-            zero_rows(a, o);
+            zero_rows<NT>(a, o);
             return;
         }
-        if (lo.bits == 2) read_group<2>(a, a.cache + off, static_cast<int>(t0), o);
-        else if (lo.bits == 4) read_group<4>(a, a.cache + off, static_cast<int>(t0), o);
-        else read_group<8>(a, a.cache + off, static_cast<int>(t0), o);
+        if (lo.bits == 2) read_group<2, NT>(a, a.cache + off, static_cast<int>(t0), o);
+        else if (lo.bits == 4) read_group<4, NT>(a, a.cache + off, static_cast<int>(t0), o);
+        else read_group<8, NT>(a, a.cache + off, static_cast<int>(t0), o);
         return;
     }
     const uint8_t* base = a.cache + lo.data_off + unit_index(lo, a.layer, b, h) * lo.unit;
     if (o.hi > n) {                             // the rows past the sequence's tokens
         Rows<T> past = o;
         past.lo = n;
-        zero_rows(a, past);
+        zero_rows<NT>(a, past);
         o.hi = n;
     }
-    if (lo.scheme == KVQ_SCHEME_INT8) read_rows<true>(a, base, o);
-    else if (lo.scheme == KVQ_SCHEME_INT4) read_rows<false>(a, base, o);
-    else read_fp8(a, base, reinterpret_cast<const float*>(a.cache + lo.scales_off) + ((int64_t)a.layer * lo.H + h) * 2, o);
+    if (lo.scheme == KVQ_SCHEME_INT8) read_rows<true, NT>(a, base, o);
+    else if (lo.scheme == KVQ_SCHEME_INT4) read_rows<false, NT>(a, base, o);
+    else read_fp8<NT>(a, base, reinterpret_cast<const float*>(a.cache + lo.scales_off) + ((int64_t)a.layer * lo.H + h) * 2, o);
 }
 
 }  // namespace
@@ -367,10 +365,17 @@ extern "C" int kvq_read_tokens(const kvq_config* cfg, void* cache, int32_t layer
         a.out[0] = k_out ? static_cast<uint8_t*>(k_out) + rows : nullptr;
         a.out[1] = v_out ? static_cast<uint8_t*>(v_out) + rows : nullptr;
         const dim3 grid(static_cast<unsigned>((count + (int64_t)a.tile - 2) / a.tile + 1), a.lo.H, now);
-        if (out_dtype == KVQ_DTYPE_BF16)
-            kvq::k_read<__nv_bfloat16><<<grid, kvq::kReadThreads, 0, s>>>(a);
-        else
-            kvq::k_read<float><<<grid, kvq::kReadThreads, 0, s>>>(a);
+        // many blocks: small ones, more of them on an SM at different points of their work (a
+        // 2-bit layer of 8 x 4096 tokens: 40 us with 64 threads, 43 with 128, 59 with 256); few:
+        // large ones, for latency (257 tokens of one sequence: 10.4, 8.3 and 7.3)
+        const bool many = (int64_t)grid.x * grid.y * grid.z >= 8 * 152;
+        if (out_dtype == KVQ_DTYPE_BF16) {
+            if (many) kvq::k_read<__nv_bfloat16, 64><<<grid, 64, 0, s>>>(a);
+            else kvq::k_read<__nv_bfloat16, 256><<<grid, 256, 0, s>>>(a);
+        } else {
+            if (many) kvq::k_read<float, 64><<<grid, 64, 0, s>>>(a);
+            else kvq::k_read<float, 256><<<grid, 256, 0, s>>>(a);
+        }
         if (cudaGetLastError() != cudaSuccess) return KVQ_ERR_CUDA;
     }
     return KVQ_OK;

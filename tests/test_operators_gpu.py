@@ -154,6 +154,29 @@ def test_read_one_of_keys_and_values_and_into_given_tensors(K):
     assert torch.equal(out[0], before[0]) and torch.equal(out[3], before[3]) and torch.equal(out[1:3], k)
 
 
+@pytest.mark.parametrize("case", [
+    dict(bits=2, group_k=16, group_v=16, head_dim=64), dict(bits=4, group_k=48, group_v=32, outliers=2, head_dim=128),
+    dict(bits=8, group_k=32, group_v=64, head_dim=256), dict(scheme="int8", head_dim=32), dict(scheme="int4", head_dim=128),
+    dict(scheme="fp8", head_dim=64), dict(scheme="fp8e5m2", head_dim=256)], ids=str)
+def test_read_of_many_tiles_is_the_read_of_its_pieces(K, case):
+    """Large reads run other blocks than small ones (test_read_is_the_oracles_dequantised_value)."""
+    scheme = case.get("scheme", "kivi")
+    B, H, n, D = 3, 12, 4000, case["head_dim"]
+    kw = {x: case[x] for x in ("bits", "group_k", "group_v", "outliers") if x in case}
+    cache = K.QuantizedKVCache(K.make_config(scheme, 1, B, H, H, D, n, residual=37 if scheme == "kivi" else 0, **kw))
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    k, v = (torch.randn(B, n, H, D, generator=gen, device="cuda").to(BF16) for _ in range(2))
+    scales = torch.full((H, 2), 0.01, device="cuda")
+    counts = torch.tensor([n, n - 133, 17], dtype=torch.int32, device="cuda")
+    cache.append(0, k, v, n_valid=counts, fp8_scales=scales)
+    for dtype in ("bf16", "f32"):
+        whole = cache.read(0, count=n, dtype=dtype)
+        for b, first in ((0, 0), (0, n - 100), (1, n - 200), (2, 0), (1, 1111)):
+            piece = cache.read(0, first=first, count=100, seq_begin=b, seq_count=1, dtype=dtype)
+            for w, x in zip(whole, piece):
+                assert torch.equal(w[b, first:first + 100], x[0])
+
+
 def test_read_reports_a_page_outside_the_pool(K):
     case = dict(bits=2, group_k=32, group_v=32, lengths=(300, 300), max_tokens=320, paged=2)
     p, _ = make(case)
@@ -513,7 +536,7 @@ def rope64(x, pos, w, R, layout, magnitude, transpose):
 @pytest.mark.parametrize("dtype", [BF16, torch.float32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("layout", ["half", "interleaved"])
 @pytest.mark.parametrize("tokens,Hq,H,D,R", [(1, 1, 1, 2, 2), (7, 32, 8, 128, 128), (33, 3, 1, 96, 48), (5, 8, 8, 64, 2),
-                                             (3, 1, 2, 80, 20), (130, 2, 1, 256, 256), (4, 5, 1, 1024, 256),
+                                             (3, 1, 2, 80, 20), (700, 2, 1, 256, 256), (4, 5, 1, 1024, 256),
                                              (9, 4, 2, 7, 6)])
 def test_rope(K, dtype, layout, tokens, Hq, H, D, R):
     gen = torch.Generator().manual_seed(tokens)
