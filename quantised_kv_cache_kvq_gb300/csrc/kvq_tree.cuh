@@ -1225,10 +1225,11 @@ __global__ void __launch_bounds__(TreeShape<N, D>::kThreads, TreeShape<N, D>::kB
         if (tid == NT - 1) sh.start = base;
         __syncthreads();
         const int b = b0 + tid;
+        const int64_t from = sh.start;                  // (read before the scan's barriers: it is written again behind them)
         int64_t sum;
         if (b < lo.B) seq = tree_seq(a, b, N);
         mine = b < lo.B ? H * tree_head_tiles(a, seq) : 0;
-        at = sh.start + block_scan<NT>(mine, sh.scan, &sum);
+        at = from + block_scan<NT>(mine, sh.scan, &sum);
     }
     tmem_fence_before();
     __syncthreads();
