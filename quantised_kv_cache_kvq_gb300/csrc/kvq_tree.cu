@@ -83,7 +83,7 @@ int tree_plan(const kvq_config* cfg, int nodes, TreePlan* p) {
     p->stages = left >= 2 * p->stage ? 2 : left >= p->stage ? 1 : 0;
     p->stage_at = static_cast<int>(tiles - (p->share ? 256 * p->N : 0));
     if (p->stages == 0) {
-        if (lo.scheme != KVQ_SCHEME_KIVI) return KVQ_ERR_UNSUPPORTED;
+        if (lo.scheme != KVQ_SCHEME_KIVI || D != 256) return KVQ_ERR_UNSUPPORTED;
         p->stage = 0;
     }
     p->RT = (p->rows + p->N - 1) / p->N;
@@ -103,8 +103,7 @@ int launch_tree(TreeArgs& a, int N, cudaStream_t st) {
     if (is_fp8(a.lo.scheme))
         return D == 32 ? launch_tree_fp8_d32(a, N, st) : D == 64 ? launch_tree_fp8_d64(a, N, st)
              : D == 128 ? launch_tree_fp8_d128(a, N, st) : launch_tree_fp8_d256(a, N, st);
-    if (a.stages == 0)
-        return D == 256 ? launch_tree_inplace_d256(a, N, st) : KVQ_ERR_UNSUPPORTED;
+    if (a.stages == 0) return launch_tree_inplace_d256(a, N, st);    // (of 256 channels: tree_plan)
     switch (a.lo.bits) {
         case 2:
             return D == 64 ? launch_tree_kivi2_d64(a, N, st) : D == 128 ? launch_tree_kivi2_d128(a, N, st)
