@@ -135,7 +135,7 @@ class QuantizedKVCache:
         [kv_heads][head_dim]; mask: bool or uint8 [batch][nodes][nodes] (None: a chain);
         n_nodes: int32 [batch] or None.  Returns bf16 [batch][nodes][q_heads][head_dim].
         workspace: tree_workspace(nodes), by default one that the cache keeps for each number
-        of nodes."""
+        of nodes (calls on several streams, and graphs replayed side by side, need their own)."""
         import torch
         c, device, bf16 = self.cfg, self.device, torch.bfloat16
         batch, heads, D = c.batch, c.kv_heads, c.head_dim
@@ -151,6 +151,8 @@ class QuantizedKVCache:
             if workspace is None:
                 workspace = self._tree_workspaces.get(nodes)
                 if workspace is None:
+                    if torch.cuda.is_current_stream_capturing():    # (it would be the graph's memory)
+                        raise ValueError("tree_decode: a captured call needs a workspace made before the capture")
                     workspace = self._tree_workspaces[nodes] = self.tree_workspace(nodes)
             if out is None:
                 out = torch.empty(q.shape, dtype=bf16, device=device)

@@ -476,6 +476,27 @@ def test_tree_is_repeatable_and_captured(K):
     assert torch.equal(graphs[0][2], a2)
 
 
+def test_tree_captured_before_its_workspace_is_made_is_refused(K):
+    """A workspace that the cache keeps is not made of a graph's memory."""
+    p, gen = make(dict(bits=2, lengths=(200, 100), max_tokens=208))
+    cache = wrap(K, p)
+    q, dk, dv, mask = (x.cuda() for x in drafts(p, 5, gen))
+    out = torch.zeros_like(q)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out.fill_(1.0)
+        with pytest.raises(ValueError, match="before the capture"):
+            cache.tree_decode(0, q, dk, dv, mask, out=out)
+    want = cache.tree_decode(0, q, dk, dv, mask)            # makes it
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        cache.tree_decode(0, q, dk, dv, mask, out=out)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and cache.status() == 0
+
+
 def test_tree_from_page_locked_host_memory_on_another_stream(K):
     p, gen = make(dict(bits=2, lengths=(200, 100), max_tokens=208))
     cache = wrap(K, p)
