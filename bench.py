@@ -127,7 +127,7 @@ def decode_bytes(w, lengths):
 
 
 DECODE_SOURCES = ("kvq_api.cu", "kvq_decode.cuh", "kvq_decode_rows.cu", "kvq_internal.cuh", "kvq_launch.h",
-                  "kvq_rope.cuh")
+                  "kvq_rope.cuh", "kvq_rope_angle.cuh")
 SCHEME_SOURCES = {0: tuple("kvq_decode_kivi%d%s.cu" % (b, v) for b in (2, 4, 8)
                             for v in ("", "_steal", "_paged", "_paged_steal", "_sparse", "_sparse_paged", "_rope",
                                       "_rope_paged"))
