@@ -12,18 +12,33 @@
 // runs, takes the scores out of TMEM, writes the weights to shared memory and issues their
 // product, which runs under the next tile's keys.  Two blocks share an SM where their tiles fit
 // (heads of up to 128 channels, up to 64 columns), so that one computes while the other waits.
-// (Warps in roles that hand tiles on through mbarriers -- copy, check, keys, values, product,
-// softmax -- measured slower: 133 us against the figure below for 16 drafts over a 2-bit layer
-// of 8 x 4096 tokens.  The roles' code, side by side, missed the instruction cache, their
-// waits took issue slots, and 20 to 24 warps left too few registers.)
+//
+// Measured (a call: this kernel and the join of its parts; 32 query and 8 KV heads of 128):
+//   16 drafts, 2-bit, 8 x 4096 tokens       53 us   (its bytes take 4.6 us at the copy bandwidth)
+//   32 drafts, 4-bit, 131072 tokens        178 us   (its products take 35 us at the dense bf16 rate)
+//   8 drafts, FP8, 64 x 8192 tokens        333 us   (its bytes take 160 us)
+// The kernel issues instructions in 33 to 52% of its cycles, and the tensor pipe is busy in 8 to
+// 17%: a tile is a chain of short phases (unpack, product, unpack, softmax, product), each of a
+// few hundred instructions a warp behind a barrier, and 128 registers a thread allow two blocks
+// of 8 warps to fill each other's gaps.  Measured slower: warps in roles (copy, keys, values,
+// product, softmax) that hand tiles on through mbarriers (133 us where the phases took 113: the
+// roles' code, side by side, missed the instruction cache, their waits took issue slots, and 20
+// to 24 warps left too few registers); 16 warps of 64 registers a block (78 us for 53: spills);
+// row tiles of 64 columns in place of 128, so that two blocks fit (237 us for 192); the weights
+// written before the vote on the references, to save its barrier (FP8 349 us for 333).
 //
 // Softmax, in base 2.  A token's value row is stored in binary16 as v 2^-e (or as its code),
 // v = stored * s; the weight that multiplies it is P = 2^(x + log2 s - m) with a running
 // reference m per column: 8 under the largest x + log2 s seen, so that P <= 2^8 and weights
-// down to 2^-22 of the largest keep binary16's 11 bits.  m moves only when some entry of a
-// tile reaches 2^15 above it (every first tile; hardly ever later): then O^T is rescaled in
-// TMEM.  The sum l takes P / s in binary32, per thread, and is joined at the end; O / l is the
-// output.  A masked entry has x = -infinity and takes no part in anything.
+// down to 2^-22 of the largest keep binary16's 11 bits.  m is set on a segment's first tile
+// and moves later only when some entry of a tile reaches 2^15 above it: then O^T is rescaled
+// in TMEM.  The sum l takes P / s in binary32, per thread, and is joined at the end; O / l is
+// the output.  A masked entry has x = -infinity and takes no part in anything.
+//
+// Roundings to 16 bits: a product's operands only.  Queries and raw rows (bf16, 8 bits) go into
+// binary16's 11 exactly, under a power of two, but for what lies 2^-30 below their largest;
+// a KIVI key or value is rounded once behind its fused multiply-add, a turned key once more;
+// FP8, INT8 and INT4 codes are exact; a weight is rounded once, by 2^-11 of itself.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -42,7 +57,7 @@ constexpr float kReach = 15.0f;         // P may grow to 2^15 before the referen
 
 // What a kernel unpacks: KIVI records of 2, 4 or 8 bits, KIVI records read where they lie (any
 // bits; those that do not fit next to the operand tiles), INT8 and INT4 rows, FP8 tiles.  The
-// kinds are kernels of their own: together in one, their code costs every role registers.
+// kinds are kernels of their own: together in one, their code costs every path registers.
 enum TreeKind { kKivi2 = 2, kKivi4 = 4, kKivi8 = 8, kInPlace = 16, kRows = 32, kFp8 = 64 };
 
 struct TreeArgs {
@@ -878,6 +893,7 @@ struct TreeShared {
     int seen[N];                    // it has a reference
     float fac[N], part[4][N];       // per column: factors; per quadrant: maxima, sums
     float kf[128], vl[128];         // a raw row's score factor and log2 of its value scale
+    float kscale, vscale, vscale_log;       // FP8: the KV head's scales, log2 of the values'
     float wt[D / 2];                // rotary frequencies in the order of the key tile
     int64_t scan[32], start;
     uint64_t stage_full[2], s_full, pv_done;
@@ -927,6 +943,12 @@ __device__ __noinline__ float2 load_queries(const TreeArgs& a, int row0, int row
     if (tid == 0) {
         sh.qtop = -200;
         sh.qlow = 200;
+        if constexpr (KIND == kFp8) {
+            const float* sc = fp8_scale(a, w.h);
+            sh.kscale = sc[0];
+            sh.vscale = sc[1];
+            sh.vscale_log = fmaxf(fast_log2(fabsf(sc[1])), -110.0f);    // (a scale of 0 belongs to codes of 0)
+        }
     }
     __syncthreads();
     // (at most one octet per warp: 16 columns have 2, 64 have 8 of 8 warps, 128 have 16 of 16)
@@ -1364,8 +1386,8 @@ __global__ void __launch_bounds__(TreeShape<N, D>::kThreads, TreeShape<N, D>::kB
                         f = pow2i(ke);
                         lv = static_cast<float>(ve);
                     } else if constexpr (fp8) {
-                        f = fp8_scale(a, w.h)[0];
-                        lv = fmaxf(fast_log2(fabsf(fp8_scale(a, w.h)[1])), -110.0f);
+                        f = sh.kscale;
+                        lv = sh.vscale_log;
                     } else {
                         const float* sc = reinterpret_cast<const float*>(raw + 256 * row_bytes);
                         f = sc[tok];
@@ -1388,7 +1410,7 @@ __global__ void __launch_bounds__(TreeShape<N, D>::kThreads, TreeShape<N, D>::kB
                         }
                     } else {
                         const uint8_t* vraw = raw + 128 * row_bytes;
-                        if constexpr (fp8) fp8_values<D, CT>(vraw, cnt, lo.scheme == KVQ_SCHEME_FP8_E4M3, fp8_scale(a, w.h)[1] < 0.0f, vt, tid);
+                        if constexpr (fp8) fp8_values<D, CT>(vraw, cnt, lo.scheme == KVQ_SCHEME_FP8_E4M3, sh.vscale < 0.0f, vt, tid);
                         else rows_codes<D, CT>(vraw, cnt, 1, lo.scheme == KVQ_SCHEME_INT8, vt, tid);
                     }
                 }
