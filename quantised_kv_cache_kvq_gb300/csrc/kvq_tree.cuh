@@ -896,18 +896,20 @@ struct TreeShared {
     float kscale, vscale, vscale_log;       // FP8: the KV head's scales, log2 of the values'
     float wt[D / 2];                // rotary frequencies in the order of the key tile
     int64_t scan[32], start;
-    uint64_t stage_full[2], s_full, pv_done;
+    uint64_t stage_full[2], keys_full[2], s_full, pv_done;   // (keys_full: rows and FP8, whose keys come apart)
     const uint8_t* recs[8];         // records read in place
     int qtop, qlow;                 // exponents of the largest and the smallest query
     uint32_t tmem, top[2];
     TreeWalk walk;                  // the segment
     int more;
     // the next packed tile to bring in: its segment, where it lies, what is left of the segment's
-    // packed part (KIVI: groups; others: tokens), its first group
+    // packed part (KIVI: groups; others: tokens); paged: the table's entry, the group in its page, the
+    // page (negative: not looked up yet)
     TreeWalk ahead;
     const uint8_t* ahead_src;
-    int ahead_left, ahead_group;
+    int ahead_left, ahead_entry, ahead_in, ahead_page;
     uint32_t ahead_slot;
+    bool keys_sent;                 // rows and FP8: the next tile's keys are on their way
     int dead, odd;                  // a wait gave up; a draft's value is not finite
 };
 
@@ -1128,9 +1130,14 @@ __device__ __noinline__ void copy_segment(const TreeArgs& a, TreeShared<N, D>& s
         const uint8_t* base = a.cache + a.lo.data_off + unit_index(a.lo, a.layer, w.b, w.h) * a.lo.unit;
         const int all = w.s.qn < end * a.TT ? w.s.qn : end * a.TT, rest = all - w.first * a.TT;
         if constexpr (KIND <= kInPlace) {
-            sh.ahead_group = w.first * a.TG;
+            const int group = w.first * a.TG;
             sh.ahead_left = rest / a.lo.G;
-            sh.ahead_src = base + (int64_t)sh.ahead_group * a.lo.rec;
+            sh.ahead_src = base + (int64_t)group * a.lo.rec;
+            if (a.lo.PG > 0) {
+                sh.ahead_entry = group / a.lo.PG;
+                sh.ahead_in = group - sh.ahead_entry * a.lo.PG;
+                sh.ahead_page = -1;
+            }
         } else {
             sh.ahead_left = rest;
             sh.ahead_src = base + (int64_t)w.first * 128 * (a.lo.scheme == KVQ_SCHEME_INT4 ? D / 2 : D);
@@ -1138,34 +1145,61 @@ __device__ __noinline__ void copy_segment(const TreeArgs& a, TreeShared<N, D>& s
         return;
     }
 }
-// `ng` group records from the pages that sh.ahead's block table names.
+// `ng` group records from the pages that sh.ahead's block table names: a copy for each page (a
+// head's records lie one after another in it), whose entry is looked up once.
 template <int N, int D>
 __device__ __noinline__ void copy_pages(const TreeArgs& a, TreeShared<N, D>& sh, uint8_t* to, uint64_t* bar, int ng) {
     const Layout& lo = a.lo;
-    const int32_t* table = lo.table + (int64_t)sh.ahead.b * lo.MP;
-    int pg = sh.ahead_group / lo.PG, in = sh.ahead_group - pg * lo.PG;
-    for (int g = 0; g < ng; ++g) {
-        int32_t page = table[pg];
-        if (page < 0 || page >= lo.NP) {        // outside the pool: page 0 in its place, reported
-            atomicOr(reinterpret_cast<uint32_t*>(a.ws), KVQ_STATUS_BAD_PAGE);
-            page = 0;
+    while (ng > 0) {
+        int in = sh.ahead_in, page = sh.ahead_page;
+        if (page < 0) {
+            page = lo.table[(int64_t)sh.ahead.b * lo.MP + sh.ahead_entry];
+            if (page < 0 || page >= lo.NP) {    // outside the pool: page 0 in its place, reported
+                atomicOr(reinterpret_cast<uint32_t*>(a.ws), KVQ_STATUS_BAD_PAGE);
+                page = 0;
+            }
+            sh.ahead_page = page;
         }
-        bulk_copy_g2s(to + g * lo.rec,
-                      a.cache + lo.data_off + (int64_t)page * lo.page + (((int64_t)a.layer * lo.H + sh.ahead.h) * lo.PG + in) * lo.rec,
-                      lo.rec, bar);
-        if (++in == lo.PG) {
+        const int run = ng < lo.PG - in ? ng : lo.PG - in;
+        bulk_copy_g2s(to, a.cache + lo.data_off + (int64_t)page * lo.page + (((int64_t)a.layer * lo.H + sh.ahead.h) * lo.PG + in) * lo.rec,
+                      run * lo.rec, bar);
+        to += run * lo.rec;
+        ng -= run;
+        in += run;
+        if (in == lo.PG) {
             in = 0;
-            ++pg;
+            ++sh.ahead_entry;
+            sh.ahead_page = -1;
         }
+        sh.ahead_in = in;
     }
 }
-// Brings the block's next packed tile, if there is one, to the next stage; one thread.
+// Brings the block's next packed tile, if there is one, to the next stage; one thread.  KIVI: its
+// records.  Rows and FP8: its keys (copy_keys), then its values and scales (copy_next), each as
+// soon as the stage's last ones are read.
+template <int N, int D, int KIND>
+__device__ __forceinline__ bool copy_ready(const TreeArgs& a, TreeShared<N, D>& sh) {
+    if (sh.ahead_left == 0) copy_segment<N, D, KIND>(a, sh, true);
+    return sh.ahead_left > 0 && !*static_cast<volatile int*>(&sh.dead);
+}
+template <int N, int D, int KIND>
+__device__ __forceinline__ void copy_keys(const TreeArgs& a, TreeShared<N, D>& sh, uint8_t* stage) {
+    sh.keys_sent = copy_ready<N, D, KIND>(a, sh);
+    if (!sh.keys_sent) return;
+    const int row_bytes = a.lo.scheme == KVQ_SCHEME_INT4 ? D / 2 : D, left = sh.ahead_left;
+    const uint32_t bytes = static_cast<uint32_t>((((left < 128 ? left : 128) + 15) & ~15) * row_bytes), slot = sh.ahead_slot;
+    mbar_arrive_expect_tx(&sh.keys_full[slot], bytes);
+    bulk_copy_g2s(stage + slot * a.stage_bytes, sh.ahead_src, bytes, &sh.keys_full[slot]);
+}
 template <int N, int D, int KIND>
 __device__ __forceinline__ void copy_next(const TreeArgs& a, TreeShared<N, D>& sh, uint8_t* stage) {
     const Layout& lo = a.lo;
-    if (sh.ahead_left == 0) copy_segment<N, D, KIND>(a, sh, true);
+    if constexpr (KIND <= kInPlace) {
+        if (!copy_ready<N, D, KIND>(a, sh)) return;
+    } else {
+        if (sh.ahead_left <= 0 || !sh.keys_sent) return;
+    }
     const int left = sh.ahead_left;
-    if (left <= 0 || *static_cast<volatile int*>(&sh.dead)) return;
     const uint32_t slot = sh.ahead_slot;
     if (a.stages == 2) sh.ahead_slot = slot ^ 1;
     uint8_t* to = stage + slot * a.stage_bytes;
@@ -1180,15 +1214,13 @@ __device__ __forceinline__ void copy_next(const TreeArgs& a, TreeShared<N, D>& s
             bulk_copy_g2s(to, src, ng * lo.rec, bar);
         else
             copy_pages(a, sh, to, bar, ng);
-        sh.ahead_group += a.TG;
     } else {
         const int cnt = left < 128 ? left : 128, c16 = (cnt + 15) & ~15;
         const int row_bytes = lo.scheme == KVQ_SCHEME_INT4 ? D / 2 : D;
         sh.ahead_left = left - cnt;
         sh.ahead_src = src + 128 * row_bytes;
         const uint32_t bytes = static_cast<uint32_t>(c16 * row_bytes);
-        mbar_arrive_expect_tx(bar, 2 * bytes + (KIND == kRows ? 8 * c16 : 0));
-        bulk_copy_g2s(to, src, bytes, bar);
+        mbar_arrive_expect_tx(bar, bytes + (KIND == kRows ? 8 * c16 : 0));
         bulk_copy_g2s(to + 128 * row_bytes, src + (int64_t)lo.T16 * row_bytes, bytes, bar);
         if constexpr (KIND == kRows) {          // the scales: 4 bytes a row from the unit's codes' end on
             const uint8_t* base = a.cache + lo.data_off + unit_index(lo, a.layer, sh.ahead.b, sh.ahead.h) * lo.unit;
@@ -1221,6 +1253,8 @@ __global__ void __launch_bounds__(TreeShape<N, D>::kThreads, TreeShape<N, D>::kB
     if (tid == 32) {
         mbar_init(&sh.stage_full[0], 1);
         mbar_init(&sh.stage_full[1], 1);
+        mbar_init(&sh.keys_full[0], 1);
+        mbar_init(&sh.keys_full[1], 1);
         mbar_init(&sh.s_full, 1);
         mbar_init(&sh.pv_done, 1);
         sh.dead = 0;
@@ -1277,7 +1311,10 @@ __global__ void __launch_bounds__(TreeShape<N, D>::kThreads, TreeShape<N, D>::kB
             sh.ahead = w;
             sh.ahead_slot = 0;
             copy_segment<N, D, KIND>(a, sh, false);
-            for (int i = 0; i < a.stages; ++i) copy_next<N, D, KIND>(a, sh, stage);
+            for (int i = 0; i < a.stages; ++i) {
+                if constexpr (!kivi) copy_keys<N, D, KIND>(a, sh, stage);
+                copy_next<N, D, KIND>(a, sh, stage);
+            }
         }
         uint32_t it = 0, used = 0;              // tiles, and packed tiles, so far
         do {
@@ -1302,7 +1339,7 @@ __global__ void __launch_bounds__(TreeShape<N, D>::kThreads, TreeShape<N, D>::kB
                 const bool packed = tile < packed_end;
                 const int cnt = packed ? w.packed_count(a, tile) : w.raw_count(tile);
                 int ke = 0, ve = 0;                                     // KIVI: exponents outside binary16
-                const uint32_t slot = slot_of(used);
+                const uint32_t slot = slot_of(used), turn = turn_of(used);
                 const uint8_t* raw = stage + slot * a.stage_bytes;
                 PackedTile<staged_tiles> t;
                 t.base = raw;
@@ -1323,7 +1360,7 @@ __global__ void __launch_bounds__(TreeShape<N, D>::kThreads, TreeShape<N, D>::kB
                     __syncthreads();
                 } else {
                     if constexpr (staged_tiles) {
-                        wait(&sh.stage_full[slot], turn_of(used));
+                        wait(kivi ? &sh.stage_full[slot] : &sh.keys_full[slot], turn);
                     } else {
                         // records too large to pass through shared memory next to the tiles
                         if (tid < 8 && tid * lo.G < cnt) {
@@ -1362,6 +1399,10 @@ __global__ void __launch_bounds__(TreeShape<N, D>::kThreads, TreeShape<N, D>::kB
                         }
                     }
                 }
+                // the tile's key bytes are read
+                if constexpr (!kivi) {
+                    if (packed && warp == CT / 32 - 1 && elect_one()) copy_keys<N, D, KIND>(a, sh, stage);
+                }
                 if (warp == 0 && elect_one()) {
                     tmem_fence_after();
                     const uint64_t dk = mma_desc(smem_addr(kt), D / 8 * kCoreBytes), dq = mma_desc(smem_addr(qt), D / 8 * kCoreBytes);
@@ -1372,6 +1413,7 @@ __global__ void __launch_bounds__(TreeShape<N, D>::kThreads, TreeShape<N, D>::kB
                     mma_commit(&sh.s_full);
                 }
                 __syncwarp();
+                if (!kivi && packed) wait(&sh.stage_full[slot], turn);      // its values and scales
                 // ---- this thread's token: factor of its scores, log2 of its values' scale
                 const int tok = packed && !rows_scheme ? packed_token(row) : row;
                 const bool valid = tok < cnt, masked = cnt < 128 || !packed;
@@ -1563,7 +1605,10 @@ __global__ void __launch_bounds__(TreeShape<N, D>::kThreads, TreeShape<N, D>::kB
         } while (sh.more);
         // where a wait gave up, the copies in flight land before the block ends
         if (staged_tiles && tid == 0 && sh.dead)
-            for (uint32_t i = used; i < used + a.stages; ++i) mbar_wait_asleep(&sh.stage_full[slot_of(i)], turn_of(i) & 1);
+            for (uint32_t i = used; i < used + a.stages; ++i) {
+                if (!kivi) mbar_wait_asleep(&sh.keys_full[slot_of(i)], turn_of(i) & 1);
+                mbar_wait_asleep(&sh.stage_full[slot_of(i)], turn_of(i) & 1);
+            }
     }
     __syncthreads();
     if (warp == 0) tmem_free(tm_s, S::kCols);
