@@ -16,7 +16,7 @@
 // Measured (a call: this kernel and the join of its parts; 32 query and 8 KV heads of 128):
 //   16 drafts, 2-bit, 8 x 4096 tokens       53 us   (its bytes take 4.6 us at the copy bandwidth)
 //   32 drafts, 4-bit, 131072 tokens        178 us   (its products take 35 us at the dense bf16 rate)
-//   8 drafts, FP8, 64 x 8192 tokens        333 us   (its bytes take 160 us)
+//   8 drafts, FP8, 64 x 8192 tokens        306 us   (its bytes take 160 us)
 // The kernel issues instructions in 33 to 52% of its cycles, and the tensor pipe is busy in 8 to
 // 17%: a tile is a chain of short phases (unpack, product, unpack, softmax, product), each of a
 // few hundred instructions a warp behind a barrier, and 128 registers a thread allow two blocks
@@ -774,7 +774,7 @@ struct TreeShape {
     static constexpr uint32_t kCols = kTmem <= 32 ? 32 : kTmem <= 64 ? 64 : kTmem <= 128 ? 128 : kTmem <= 256 ? 256 : 512;
     // shared memory: K, V (the product reads 128 channel rows of it), Q, P, then the stages
     static constexpr int kVBytes = D > 128 ? 65536 : 32768;
-    static constexpr int kK = 0, kV = 256 * D, kQ = kV + kVBytes, kP = kQ + 2 * N * D, kStage = kP + 256 * N;
+    static constexpr int kK = 0, kV = 256 * D, kQ = kV + kVBytes, kP = kQ + 2 * N * D;
 };
 
 __device__ __forceinline__ bool elect_one() {
@@ -805,11 +805,6 @@ __device__ __forceinline__ uint64_t pack2(float x, float y) {
 }
 __device__ __forceinline__ void unpack2(uint64_t v, float* x, float* y) {
     asm("mov.b64 {%0, %1}, %2;" : "=f"(*x), "=f"(*y) : "l"(v));
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
 }
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     uint64_t r;
