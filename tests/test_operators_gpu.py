@@ -411,6 +411,24 @@ def test_tree_of_more_sequences_than_threads(K, gqa, nodes):
         assert not got[b, max(c, 0):].any()
 
 
+@pytest.mark.parametrize("case", [dict(scheme="int8", head_dim=64), dict(scheme="int4", head_dim=32), dict(scheme="fp8", head_dim=128),
+                                  dict(bits=2, head_dim=64, group_k=16, group_v=16, residual=20, paged=3)], ids=str)
+def test_tree_of_many_short_sequences(K, case):
+    """Several sequences to a block, some empty or without drafts: its copies run ahead from one to
+    the next."""
+    gen = torch.Generator().manual_seed(8)
+    lengths = torch.randint(0, 300, (200,), generator=gen).tolist()
+    lengths[7:12] = [0, 0, 299, 0, 128]
+    p, gen = make(dict(case, kv_heads=4, q_heads=8, lengths=lengths, max_tokens=300))
+    counts = torch.randint(0, 4, (200,), generator=gen).tolist()
+    q, dk, dv, mask = drafts(p, 3, gen)
+    cache = wrap(K, p)
+    got = cache.tree_decode(0, q.cuda(), dk.cuda(), dv.cuda(), mask.cuda(),
+                            torch.tensor(counts, dtype=torch.int32, device="cuda")).float().cpu().numpy()
+    ref, tol = tree64(p, 0, q, dk, dv, mask.numpy(), counts, 1.0 / math.sqrt(p.kw["head_dim"]))
+    assert (np.abs(got - ref) <= tol).all() and cache.status() == 0
+
+
 def test_tree_replayed_over_a_growing_cache(K):
     p, gen = make(dict(bits=4, lengths=(250, 60), max_tokens=900))
     cache = wrap(K, p)
