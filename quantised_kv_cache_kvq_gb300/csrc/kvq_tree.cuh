@@ -37,8 +37,8 @@
 //
 // Roundings to 16 bits: a product's operands only.  Queries and raw rows (bf16, 8 bits) go into
 // binary16's 11 exactly, under a power of two, but for what lies 2^-30 below their largest;
-// a KIVI key or value is rounded once behind its fused multiply-add, a turned key once more;
-// FP8, INT8 and INT4 codes are exact; a weight is rounded once, by 2^-11 of itself.
+// a KIVI key or value is rounded once, behind its fused multiply-add, a turned key behind the
+// turn; FP8, INT8 and INT4 codes are exact; a weight is rounded once, by 2^-11 of itself.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -739,21 +739,57 @@ __device__ __noinline__ void prefetch_rows(const TreeArgs& a, int b, int h, int 
 // Turns the tile's cached keys by their positions: row r of the tile is token t0 + (its place),
 // rows from `rows` on stay.
 template <int D, int DT>
-__device__ __noinline__ void turn_keys(uint8_t* kt, const float* w, int64_t t0, int rows, bool packed_order, int tid) {
+__device__ __noinline__ void turn_keys(uint8_t* kt, const float* w, int64_t t0, int rows, int tid) {
     constexpr uint32_t sbo = D / 8 * kCoreBytes;
     constexpr int CH = D / 16;                  // 8-channel chunks of half a row
     for (int i = tid; i < 128 * CH; i += DT) {
         const int row = (i & 7) + 8 * (i / (8 * CH)), ch = (i >> 3) % CH;
-        const int tok = packed_order ? packed_token(row) : row;
-        if (tok >= rows) continue;
+        if (row >= rows) continue;
         uint4* pa = reinterpret_cast<uint4*>(kt + core_at(row, ch, sbo));
         uint4* pb = reinterpret_cast<uint4*>(kt + core_at(row, ch + CH, sbo));
-        const float pos = static_cast<float>(t0 + tok);
+        const float pos = static_cast<float>(t0 + row);
 #pragma unroll 1
         for (int j = 0; j < 8; ++j) {           // (one sine's code, not eight)
             __half* px = reinterpret_cast<__half*>(pa) + j;
             __half* py = reinterpret_cast<__half*>(pb) + j;
             const float x = __half2float(*px), y = __half2float(*py);
+            float sn, cs;
+            rope_sincos(__fmul_rn(pos, w[8 * ch + j]), &sn, &cs);
+            *px = __float2half_rn(x * cs - y * sn);
+            *py = __float2half_rn(y * cs + x * sn);
+        }
+    }
+}
+// A dequantised key (times `scale`) in binary32 where h is its binary16 rounding, else h: an
+// outlier lies over it.
+__device__ __forceinline__ float unrounded_key(const Layout& lo, const uint8_t* rec, int tin, int c, float scale, __half h) {
+    const __half* par = reinterpret_cast<const __half*>(rec + lo.kc + lo.vc);
+    const int bit = (tin * lo.D + c) * lo.bits;
+    const float x = scale * scaled_code((rec[bit >> 3] >> (bit & 7)) & ((1 << lo.bits) - 1), __half2float(par[c]),
+                                        __half2float(par[lo.D + c]));
+    return __half_as_ushort(__float2half_rn(x)) == __half_as_ushort(h) ? x : __half2float(h);
+}
+// The same for a KIVI tile (tokens in the packed order), from the values before their rounding
+// to binary16: a turned key is rounded once.
+template <int D, int DT, typename Tile>
+__device__ __noinline__ void turn_kivi_keys(const Layout& lo, const Tile t, uint8_t* kt, const float* w, int64_t t0, float scale, int W,
+                                            int tid) {
+    constexpr uint32_t sbo = D / 8 * kCoreBytes;
+    constexpr int CH = D / 16;
+    for (int i = tid; i < 128 * CH; i += DT) {
+        const int row = (i & 7) + 8 * (i / (8 * CH)), ch = (i >> 3) % CH, tok = packed_token(row);
+        if (tok >= t.cnt) continue;
+        uint4* pa = reinterpret_cast<uint4*>(kt + core_at(row, ch, sbo));
+        uint4* pb = reinterpret_cast<uint4*>(kt + core_at(row, ch + CH, sbo));
+        const float pos = static_cast<float>(t0 + tok);
+        const int g = tok / lo.G, tin = tok - g * lo.G;
+        const uint8_t* rec = t.rec(g);
+#pragma unroll 1
+        for (int j = 0; j < 8; ++j) {
+            __half* px = reinterpret_cast<__half*>(pa) + j;
+            __half* py = reinterpret_cast<__half*>(pb) + j;
+            const int c = place_channel(8 * ch + j, W, D);
+            const float x = unrounded_key(lo, rec, tin, c, scale, *px), y = unrounded_key(lo, rec, tin, c + D / 2, scale, *py);
             float sn, cs;
             rope_sincos(__fmul_rn(pos, w[8 * ch + j]), &sn, &cs);
             *px = __float2half_rn(x * cs - y * sn);
@@ -1094,7 +1130,7 @@ __device__ __noinline__ void kivi_keys_rest(const TreeArgs& a, const Tile t, uin
         kivi_outliers<D, DT>(a.lo, t, kt, 0, pow2i(-ke), W, tid);
         __syncthreads();
     }
-    if (a.lo.rope_base > 0.0f) turn_keys<D, DT>(kt, wt, t0, t.cnt, true, tid);
+    if (a.lo.rope_base > 0.0f) turn_kivi_keys<D, DT>(a.lo, t, kt, wt, t0, pow2i(-ke), W, tid);
 }
 // The exponents of the keys and values of a tile that may reach outside binary16 (0: they do
 // not); behind and before block barriers.
@@ -1348,7 +1384,7 @@ __global__ void __launch_bounds__(TreeShape<N, D>::kThreads, TreeShape<N, D>::kB
                     raw_rows<D, CT, KIND>(a, w.b, w.h, w.s.n, w.s.qn, r0, cnt, kt, vt, sh.kf, sh.vl, &sh.odd, tid);
                     if (rope) {
                         __syncthreads();
-                        turn_keys<D, CT>(kt, sh.wt, (int64_t)w.s.qn + r0, held < cnt ? held : cnt, false, tid);
+                        turn_keys<D, CT>(kt, sh.wt, (int64_t)w.s.qn + r0, held < cnt ? held : cnt, tid);
                     }
                     smem_to_async();
                     tmem_fence_before();
